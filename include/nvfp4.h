@@ -358,6 +358,153 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
                                int32_t n_slots, const void* p, int64_t tq, int64_t ld_p, void* o_out, int32_t ot,
                                int64_t ldo, nvfp4_stream_t stream);
 
+/* --------------------------------------------- attention over the cache ----
+ * Softmax attention in one pass over the NVFP4 cache: scores, softmax and output
+ * without the score matrix of kv_window_scores / kv_window_context in memory.  The
+ * pages give no formula for it ([TW] §四 feeds attention from the window's chunks).
+ * For query i of query head h (cache head h / (q_heads / heads)) and key j:
+ *   x = scale * sum_d q[i, h, d] * K^[j, d],        K^ = e2m1 * s * g_K + mu, unrounded;
+ *   s = softcap * tanh(x / softcap)  (softcap > 0; else s = x);
+ *   s = s - slopes[h] * |q_pos - k_pos|             (with slopes);
+ *   O[i, h, :] = sum_j softmax_j(s) V^[j, :],       V^ = e2m1 * s * g_V, unrounded;
+ *   lse[h, i] = ln sum_j exp(s), over the visible keys.  A query that sees no key gets
+ * O = 0 and lse = -inf.  O is stored as bf16 (RNE).  Products on the tensor cores in
+ * binary16 with FP32 sums: e2m1 * s is exact there, queries are scaled by a power of two
+ * a row (exact for elements down to 2^-29 of the row's largest), weights are rounded to
+ * 2^-12 of their value; softmax statistics and lse are FP32.  A slot whose g_V is below
+ * 2^-60 of the window's largest counts as zero values.  Non-finite queries propagate
+ * into their own rows.
+ *   scale    : finite.  softcap: 0 (none) or positive and finite.
+ *   slopes   : device fp32 [q_heads], nullable.
+ *   causal   : 1: a key is visible where k_pos <= q_pos;  0: everywhere.
+ *   window   : 0, or a key is visible where q_pos - k_pos < window.
+ *   prefix   : keys with k_pos < prefix are visible whatever causal and window say.
+ *   slot_pos_host : HOST [n_slots], position of each listed slot's first token (its
+ *              tokens follow one another), nullable: slots follow one another from 0.
+ *   q_pos    : position of the first query; query i is at q_pos + i, or at
+ *   q_pos_dev: device int32 [tq], nullable.  Positions are 0 .. 2^31 - 2.
+ *   q_doc, k_doc : device int32 [tq] and [Tk] (keys in list order), both or neither: a
+ *              key is visible only to queries of the same document.  A query whose number
+ *              no key has (padding) sees nothing.
+ *   workspace: device memory of kv_attention_workspace_bytes, 16-byte aligned, for this
+ *              call alone until it has run (two captured graphs that may overlap need one
+ *              each).  Its contents before and after mean nothing. */
+typedef struct nvfp4_attention {
+  float scale;
+  float softcap;
+  const float* slopes;
+  int32_t causal;
+  int32_t reserved; /* must be 0 */
+  int64_t window;
+  int64_t prefix;
+  const int64_t* slot_pos_host;
+  int64_t q_pos;
+  const int32_t* q_pos_dev;
+  const int32_t* q_doc;
+  const int32_t* k_doc;
+  void* workspace;
+  size_t workspace_bytes;
+} nvfp4_attention;
+
+/* Workspace of kv_window_attention (tq queries) or kv_tree_attention (tq drafts) over a
+ * window of these token counts (HOST array). */
+nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int32_t* tokens_host, int32_t n_slots,
+                                          int64_t tq, int32_t q_heads, size_t* bytes);
+
+/* kv_window_attention — a block of queries over the window's keys.
+ *   slots_host, tokens_host, n_slots : the window, exactly as for kv_dequant_window_tokens.
+ *   q        : device bf16 [tq][q_heads][128], row pitch ldq elements (>= q_heads * 128);
+ *              q_heads a multiple of the cache's heads (shared heads).
+ *   o_out    : device bf16 [tq][q_heads][128], row pitch ldo elements.
+ *   lse_out  : device fp32 [q_heads][tq], nullable.
+ * Bases and pitches 16-byte aligned; head_dim 128; tq * q_heads / heads <= 65535 * 16.
+ * A listed slot whose recorded token count differs sets device status NVFP4_ERR_SHAPE and
+ * its keys count as masked.  Errors: INVALID_ARG, SHAPE, ALIGNMENT. */
+nvfp4_status kv_window_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
+                                 int32_t n_slots, const void* q, int64_t tq, int32_t q_heads, int64_t ldq,
+                                 const nvfp4_attention* at, void* o_out, int64_t ldo, float* lse_out,
+                                 nvfp4_stream_t stream);
+
+/* kv_tree_attention — drafted tokens that are not in the cache yet: each sees the window,
+ * itself and its ancestors.  One draft is a decode step, a chain of parents a run of new
+ * causal tokens, anything else a tree of drafts to verify in one pass.
+ *   k_new, v_new : device bf16 [drafts][heads][128], row pitch ld_new elements, used as they
+ *              are (FP32 sums).  A draft that a row does not see is not read for it.
+ *   parents  : device int32 [drafts]: the draft that draft i continues, before it in the
+ *              list, or -1 (it continues the window).  Anything else sets device status
+ *              NVFP4_ERR_SHAPE and counts as -1.
+ *   at       : scale, softcap, slopes, window, slot_pos_host, q_pos, workspace; a draft at
+ *              depth t below the window is at position q_pos + t.  causal, prefix,
+ *              q_pos_dev and the documents must be 0 or NULL.
+ * drafts <= 1024; n_slots may be 0 (no window yet).  The rest as for kv_window_attention. */
+nvfp4_status kv_tree_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
+                               int32_t n_slots, const void* q, int64_t drafts, int32_t q_heads, int64_t ldq,
+                               const void* k_new, const void* v_new, int64_t ld_new, const int32_t* parents,
+                               const nvfp4_attention* at, void* o_out, int64_t ldo, float* lse_out,
+                               nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------- layer steps ----
+ * What a transformer layer does between the GEMMs and the cache.  No counterpart on
+ * the pages: the formulas are stated here.
+ *
+ * nvfp4_rmsnorm_quantize — RMS norm, with the residual's addition before it and the
+ * NVFP4 quantization of nvfp4_quantize behind it, so that the next nvfp4_gemm reads
+ * the result:
+ *   h = RN_xt(x + residual)  (FP32 sum; h = x without a residual), stored in h_out;
+ *   r = RN_f32(1 / sqrt(sum(h^2) / cols + eps)), up to the rounding in binary64;
+ *   y = RN(RN(h * r) * weight) in FP32;  out = quantize(y).
+ *   x, residual, h_out : device [rows][cols] of xt, row pitches ldx, ldr, ldh elements;
+ *              bases and pitches 16-byte aligned.  residual and h_out are nullable;
+ *              h_out may be x or residual (the same pitch: the residual stream is then
+ *              updated in place) and overlaps neither in any other way.
+ *   weight   : device [cols] of wt (NVFP4_BF16 or NVFP4_FP32), 16-byte aligned; NULL = ones.
+ *   eps      : finite, >= 0.
+ *   gscale_in, out, amax_out : as for nvfp4_quantize, with y in x's place.  A supplied
+ *              scale takes one pass over x; without one amax_out is required and h is
+ *              read a second time.
+ * Device status NONFINITE if y holds a NaN or Inf: without gscale_in codes, scales and
+ * *out->gscale are then not written, with it they are unspecified.  Errors: INVALID_ARG,
+ * SHAPE (cols % 16, mismatched rows/cols, pitch below cols), ALIGNMENT. */
+nvfp4_status nvfp4_rmsnorm_quantize(const void* x, int32_t xt, int64_t rows, int64_t cols, int64_t ldx,
+                                    const void* residual, int64_t ldr, const void* weight, int32_t wt, float eps,
+                                    void* h_out, int64_t ldh, const float* gscale_in, const nvfp4_tensor* out,
+                                    float* amax_out, nvfp4_stream_t stream);
+
+/* Which elements of a head form a pair: NVFP4_ROPE_HALF (i, i + rot_dim / 2),
+ * NVFP4_ROPE_INTERLEAVED (2 i, 2 i + 1). */
+typedef enum { NVFP4_ROPE_HALF = 0, NVFP4_ROPE_INTERLEAVED = 1 } nvfp4_rope_layout;
+/* Frequencies of the pairs, f_i = base^(-2 i / rot_dim):
+ *   PLAIN    f_i;
+ *   LINEAR   f_i / factor (positions interpolated);
+ *   BY_PARTS interpolation by parts (Peng et al. 2023, "YaRN"): pairs that turn beta_fast
+ *            times and more over `original` positions keep f_i, pairs that turn beta_slow
+ *            times and less take f_i / factor, with a linear ramp over the pair number in
+ *            between; sine and cosine are scaled by 0.1 ln(factor) + 1. */
+typedef enum { NVFP4_ROPE_PLAIN = 0, NVFP4_ROPE_LINEAR = 1, NVFP4_ROPE_BY_PARTS = 2 } nvfp4_rope_scaling;
+
+/* Fills freq_host (HOST, rot_dim / 2 binary64 values) and *mscale for nvfp4_rope; no
+ * device work.  The caller copies the table to the device once.  factor >= 1 is read
+ * unless scaling is PLAIN; original >= 1 and beta_fast > beta_slow > 0 for BY_PARTS. */
+nvfp4_status nvfp4_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original,
+                                    double beta_fast, double beta_slow, double* freq_host, float* mscale);
+
+/* nvfp4_rope — rotary positions on the first rot_dim elements of every head:
+ *   (a, b) -> (m (a cos t - b sin t), m (a sin t + b cos t)),  t = position * freq[i],
+ * the angle's turns in binary64 (exact to 1e-7 of a turn's angle at any 32-bit position),
+ * the rest in FP32, rounded once to xt.  The elements behind rot_dim are copied.
+ *   x, y     : device [tokens][heads][head_dim] of xt, token pitches ldx, ldy elements
+ *              (>= heads * head_dim): heads of a packed q/k/v buffer, or a chunk for
+ *              kv_quant_append.  y may be x (the same pitch) and overlaps it in no other
+ *              way.  Any element alignment; 16-byte aligned bases, pitches, head_dim and
+ *              rot_dim (rot_dim / 2 for the half layout) take vector accesses.
+ *   freq     : device binary64 [rot_dim / 2];  mscale: finite factor m.
+ *   positions: device int32 [tokens], nullable: token t is then at pos0 + t.
+ * 2 <= rot_dim <= head_dim <= 4096, rot_dim even; heads * head_dim <= 2^20.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT.  Non-finite values propagate. */
+nvfp4_status nvfp4_rope(const void* x, int32_t xt, int64_t tokens, int32_t heads, int32_t head_dim, int64_t ldx,
+                        const double* freq, int32_t rot_dim, int32_t layout, float mscale, const int32_t* positions,
+                        int64_t pos0, void* y, int64_t ldy, nvfp4_stream_t stream);
+
 /* ----------------------------------------------------------- amax history ----
  * A requantizing GEMM epilogue (nvfp4_epilogue.q_out) quantizes before its own
  * max|h| is known, so it takes a supplied tensor scale (q_gscale_in) and reports

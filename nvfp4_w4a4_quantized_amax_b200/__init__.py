@@ -25,6 +25,8 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGNMENT, ERR_NONFINITE, ERR_TIMEOUT, ERR_C
 BF16, FP32 = 0, 1
 SF_ROWMAJOR, SF_MMA = 0, 1
 ACT_NONE, ACT_GELU_TANH = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
 
 _lock = threading.Lock()
 _lib = None
@@ -64,10 +66,20 @@ class nvfp4_kv_cache(ctypes.Structure):
                 ("slot_scales_bytes", ctypes.c_int64)]
 
 
+class nvfp4_attention(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("causal", ctypes.c_int32), ("reserved", ctypes.c_int32), ("window", ctypes.c_int64),
+                ("prefix", ctypes.c_int64), ("slot_pos_host", ctypes.POINTER(ctypes.c_int64)),
+                ("q_pos", ctypes.c_int64), ("q_pos_dev", ctypes.c_void_p), ("q_doc", ctypes.c_void_p),
+                ("k_doc", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = ["nvfp4_version", "nvfp4_status_string", "nvfp4_scales_bytes", "nvfp4_quantize", "nvfp4_amax",
            "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_kv_cache_bytes", "nvfp4_kv_cache_init",
            "kv_quant_append", "kv_quant_append_noalloc", "kv_dequant_window", "kv_dequant_window_tokens",
            "kv_window_scores", "kv_window_context",
+           "kv_attention_workspace_bytes", "kv_window_attention", "kv_tree_attention",
+           "nvfp4_rmsnorm_quantize", "nvfp4_rope_frequencies", "nvfp4_rope",
            "nvfp4_lora_merge", "nvfp4_amax_history_push", "nvfp4_last_cuda_error_string",
            "nvfp4_debug_gemm_fault", "nvfp4_debug_grid_barrier",
            "nvfp4_get_device_status"]
@@ -123,6 +135,23 @@ def library():
             lib.kv_window_context.restype = i32
             lib.kv_window_context.argtypes = [KV, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), i32,
                                               vp, i64, i64, vp, i32, i64, vp]
+            I32, AT = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(nvfp4_attention)
+            lib.kv_attention_workspace_bytes.restype = i32
+            lib.kv_attention_workspace_bytes.argtypes = [KV, I32, i32, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+            lib.kv_window_attention.restype = i32
+            lib.kv_window_attention.argtypes = [KV, I32, I32, i32, vp, i64, i32, i64, AT, vp, i64, vp, vp]
+            lib.kv_tree_attention.restype = i32
+            lib.kv_tree_attention.argtypes = [KV, I32, I32, i32, vp, i64, i32, i64, vp, vp, i64, vp, AT, vp, i64, vp,
+                                              vp]
+            f32, f64 = ctypes.c_float, ctypes.c_double
+            lib.nvfp4_rmsnorm_quantize.restype = i32
+            lib.nvfp4_rmsnorm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, T, vp,
+                                                   vp]
+            lib.nvfp4_rope_frequencies.restype = i32
+            lib.nvfp4_rope_frequencies.argtypes = [i32, f64, i32, f64, i64, f64, f64, ctypes.POINTER(f64),
+                                                   ctypes.POINTER(f32)]
+            lib.nvfp4_rope.restype = i32
+            lib.nvfp4_rope.argtypes = [vp, i32, i64, i32, i32, i64, vp, i32, i32, f32, vp, i64, vp, i64, vp]
             lib.nvfp4_lora_merge.restype = i32
             lib.nvfp4_lora_merge.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, ctypes.c_float, vp, i64, vp]
             lib.nvfp4_amax_history_push.restype = i32
@@ -388,6 +417,222 @@ def kv_window_context(cache: KVCache, slots: Sequence[int], tokens: Sequence[int
     _check(library().kv_window_context(ctypes.byref(cache.handle), sarr, tarr, len(slots), _ptr(p), p.shape[1],
                                        p.stride(1), _ptr(o_out), _dtype_code(o_out), o_out.stride(0),
                                        _stream(stream)), "kv_window_context")
+
+
+def _together(**tensors):
+    """Every given tensor is on one CUDA device; returns a guard that makes it the current one."""
+    import torch
+
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, other arguments are on {dev}")
+        dev = t.device
+    return torch.cuda.device(dev)
+
+
+def nvfp4_rmsnorm_quantize(x, out: NVFP4Tensor, weight=None, eps: float = 1e-6, residual=None, h_out=None,
+                           gscale_in=None, amax_out=None, stream=None):
+    """RMS norm of h = x + residual (x alone without one), NVFP4-quantized into `out`.
+
+    x, residual, h_out: bf16 or fp32 [rows, cols], one type; weight: bf16 or fp32 [cols]
+    (None: ones).  h_out receives h and may be x or residual itself.  gscale_in (fp32 [1]):
+    supplied tensor scale, one pass; without it amax_out (fp32 [1]) is required."""
+    rows, cols = _matrix(x, "x")
+    for t, name in ((residual, "residual"), (h_out, "h_out")):
+        if t is not None and (t.dtype != x.dtype or _matrix(t, name) != (rows, cols)):
+            raise ValueError(f"{name}: x's type and shape are required")
+    if weight is not None and (weight.dim() != 1 or weight.numel() != cols or not weight.is_contiguous()):
+        raise ValueError("weight: a contiguous [cols] tensor is required")
+    _scalar(gscale_in, "gscale_in")
+    _scalar(amax_out, "amax_out")
+    with _together(x=x, residual=residual, weight=weight, h_out=h_out, gscale_in=gscale_in, amax_out=amax_out,
+                   out=out.codes):
+        _check(library().nvfp4_rmsnorm_quantize(
+            _ptr(x), _dtype_code(x), rows, cols, _pitch(x), _ptr(residual), _pitch(residual), _ptr(weight),
+            _dtype_code(weight) if weight is not None else FP32, float(eps), _ptr(h_out), _pitch(h_out),
+            _ptr(gscale_in), ctypes.byref(out.c), _ptr(amax_out), _stream(stream)), "nvfp4_rmsnorm_quantize")
+
+
+def _matrix(t, name: str):
+    _rows(t, name)
+    return tuple(t.shape)
+
+
+def _pitch(t) -> int:
+    """Row pitch in elements; the stride of a tensor of at most one row means nothing."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1:].numel() + 15) // 16 * 16
+
+
+def _scalar(t, name: str):
+    import torch
+
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+        raise ValueError(f"{name}: one float32 value is required")
+
+
+class RopeTable:
+    """Rotation frequencies of nvfp4_rope, kept on the device (binary64).
+
+    scaling: "none"; "linear" (positions divided by `factor`); "by_parts" (interpolation by
+    parts for a context `factor` times the `original` one: pairs that turn `beta_fast` times
+    over it keep their frequency, pairs that turn `beta_slow` times are stretched)."""
+
+    SCALINGS = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "by_parts": ROPE_BY_PARTS}
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+        import torch
+
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling: one of {sorted(self.SCALINGS)} is required, got {scaling!r}")
+        if rot_dim < 2 or rot_dim % 2:
+            raise ValueError(f"rot_dim: an even number of elements is required, got {rot_dim}")
+        freq = (ctypes.c_double * (rot_dim // 2))()
+        mscale = ctypes.c_float()
+        _check(library().nvfp4_rope_frequencies(rot_dim, base, self.SCALINGS[scaling], factor, original, beta_fast,
+                                                beta_slow, freq, ctypes.byref(mscale)), "nvfp4_rope_frequencies")
+        self.rot_dim, self.mscale = rot_dim, mscale.value
+        self.freq = torch.tensor(list(freq), dtype=torch.float64, device=device or torch.device("cuda"))
+
+
+def _heads_view(t, name: str):
+    """[tokens, heads, head_dim] with contiguous heads; returns the shape."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: [tokens, heads, head_dim] is required")
+    n, h, d = t.shape
+    if t.numel() > 0 and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: contiguous heads and dims are required")
+    return n, h, d
+
+
+def _positions(pos, n: int, name: str):
+    """(device int32 tensor or None, first position) of an int or an int32 [n] tensor."""
+    import torch
+
+    if isinstance(pos, torch.Tensor):
+        if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != n or not pos.is_contiguous():
+            raise ValueError(f"{name}: an int or a contiguous int32 tensor of {n} positions is required")
+        return pos, 0
+    return None, int(pos)
+
+
+def nvfp4_rope(x, table: RopeTable, positions=0, y=None, layout: int = ROPE_HALF, stream=None):
+    """Rotary positions on the first table.rot_dim elements of every head of x (bf16 or fp32
+    [tokens, heads, head_dim], heads contiguous) into y (default: x itself).
+
+    positions: int32 [tokens] on the device, or the first token's position."""
+    y = x if y is None else y
+    n, h, d = _heads_view(x, "x")
+    if y.dtype != x.dtype or _heads_view(y, "y") != (n, h, d):
+        raise ValueError("y: x's type and shape are required")
+    pos, pos0 = _positions(positions, n, "positions")
+    ld = [t.stride(0) if n > 1 else h * d for t in (x, y)]
+    with _together(x=x, y=y, positions=pos, table=table.freq):
+        _check(library().nvfp4_rope(_ptr(x), _dtype_code(x), n, h, d, ld[0], _ptr(table.freq), table.rot_dim, layout,
+                                    table.mscale, _ptr(pos), pos0, _ptr(y), ld[1], _stream(stream)), "nvfp4_rope")
+
+
+def kv_attention_workspace_bytes(cache: KVCache, tokens: Sequence[int], tq: int, q_heads: int) -> int:
+    """Bytes of workspace for kv_window_attention (tq queries) or kv_tree_attention (tq drafts)
+    over a window of these token counts."""
+    n = ctypes.c_size_t()
+    tarr = (ctypes.c_int32 * len(tokens))(*tokens)
+    _check(library().kv_attention_workspace_bytes(ctypes.byref(cache.handle), tarr, len(tokens), tq, q_heads,
+                                                  ctypes.byref(n)), "kv_attention_workspace_bytes")
+    return n.value
+
+
+def _int32(t, n: int, name: str):
+    import torch
+
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} values is required")
+
+
+def _attend(where, cache, slots, tokens, q, scale, o_out, lse_out, softcap, slopes, slot_pos, q_pos, workspace, stream,
+            causal=False, window=0, prefix=0, q_doc=None, k_doc=None, k_new=None, v_new=None, parents=None):
+    import torch
+
+    if len(tokens) != len(slots) or (slot_pos is not None and len(slot_pos) != len(slots)):
+        raise ValueError("one token count (and position) per slot")
+    _bf16(q, "q")
+    _bf16(o_out, "o_out")
+    tq, heads, _ = shape = _heads_view(q, "q")
+    if shape[2] != cache.head_dim or _heads_view(o_out, "o_out") != shape:
+        raise ValueError("q, o_out: [tq, q_heads, head_dim] of the cache's head_dim is required")
+    if lse_out is not None and (lse_out.dtype != torch.float32 or lse_out.shape != (heads, tq)
+                                or not lse_out.is_contiguous()):
+        raise ValueError("lse_out: a contiguous float32 [q_heads, tq] is required")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (heads,)
+                               or not slopes.is_contiguous()):
+        raise ValueError("slopes: a contiguous float32 [q_heads] is required")
+    _int32(q_doc, tq, "q_doc")
+    _int32(k_doc, sum(tokens), "k_doc")
+    pos, pos0 = _positions(q_pos, tq, "q_pos")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is required")
+    with _together(q=q, o_out=o_out, lse_out=lse_out, slopes=slopes, q_doc=q_doc, k_doc=k_doc, q_pos=pos, k_new=k_new,
+                   v_new=v_new, parents=parents, workspace=workspace, cache=cache.buffer):
+        if workspace is None:  # on the call's stream: the allocator reuses it behind the call's work
+            nbytes = kv_attention_workspace_bytes(cache, tokens, tq, heads)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        n = len(slots)
+        sarr, tarr = (ctypes.c_int32 * n)(*slots), (ctypes.c_int32 * n)(*tokens)
+        parr = None if slot_pos is None else (ctypes.c_int64 * n)(*slot_pos)
+        at = nvfp4_attention(float(scale), float(softcap), _ptr(slopes), 1 if causal else 0, 0, window, prefix, parr,
+                             pos0, _ptr(pos), _ptr(q_doc), _ptr(k_doc), _ptr(workspace),
+                             workspace.numel() * workspace.element_size())
+        ldq, ldo = (t.stride(0) if tq > 1 else heads * shape[2] for t in (q, o_out))
+        head = (ctypes.byref(cache.handle), sarr, tarr, n, _ptr(q), tq, heads, ldq)
+        tail = (ctypes.byref(at), _ptr(o_out), ldo, _ptr(lse_out), _stream(stream))
+        if parents is None:
+            _check(library().kv_window_attention(*head, *tail), where)
+        else:
+            ld_new = k_new.stride(0) if tq > 1 else cache.heads * cache.head_dim
+            _check(library().kv_tree_attention(*head, _ptr(k_new), _ptr(v_new), ld_new, _ptr(parents), *tail), where)
+
+
+def kv_window_attention(cache: KVCache, slots: Sequence[int], tokens: Sequence[int], q, scale: float, o_out,
+                        lse_out=None, softcap: float = 0.0, slopes=None, causal: bool = False, window: int = 0,
+                        prefix: int = 0, slot_pos: Optional[Sequence[int]] = None, q_pos=0, q_doc=None, k_doc=None,
+                        workspace=None, stream=None):
+    """Softmax attention of q (bf16 [tq, q_heads, 128]) over the window, in one pass over the
+    NVFP4 cache; o_out like q, lse_out fp32 [q_heads, tq].
+
+    softcap: scores become softcap * tanh(score / softcap).  slopes (fp32 [q_heads]): minus
+    slope * distance.  causal, window (keys at most window - 1 behind), prefix (positions below
+    it always visible), q_doc / k_doc (int32, per query and per key in list order): masks.
+    slot_pos: position of each slot's first token (default: one after the other); q_pos: the
+    first query's position or an int32 [tq] tensor.  A query that sees nothing gets 0 and -inf.
+    workspace: kv_attention_workspace_bytes of it (default: allocated for the call)."""
+    _attend("kv_window_attention", cache, slots, tokens, q, scale, o_out, lse_out, softcap, slopes, slot_pos, q_pos,
+            workspace, stream, causal, window, prefix, q_doc, k_doc)
+
+
+def kv_tree_attention(cache: KVCache, slots: Sequence[int], tokens: Sequence[int], q, k_new, v_new, parents,
+                      scale: float, o_out, lse_out=None, softcap: float = 0.0, slopes=None, window: int = 0,
+                      slot_pos: Optional[Sequence[int]] = None, q_pos: int = 0, workspace=None, stream=None):
+    """Attention of drafted tokens that are not in the cache yet: each sees the window, itself
+    and its ancestors.  q (bf16 [drafts, q_heads, 128]); k_new, v_new (bf16 [drafts, heads, 128]);
+    parents (int32 [drafts]): an earlier draft, or -1.  A draft t steps below the window is at
+    position q_pos + t.  The rest as for kv_window_attention; the window may be empty."""
+    _bf16(k_new, "k_new")
+    _bf16(v_new, "v_new")
+    shape = (q.shape[0], cache.heads, cache.head_dim)
+    if _heads_view(k_new, "k_new") != shape or _heads_view(v_new, "v_new") != shape or (
+            shape[0] > 1 and k_new.stride(0) != v_new.stride(0)):
+        raise ValueError("k_new, v_new: [drafts, heads, head_dim] of one row pitch is required")
+    _int32(parents, shape[0], "parents")
+    _attend("kv_tree_attention", cache, slots, tokens, q, scale, o_out, lse_out, softcap, slopes, slot_pos, int(q_pos),
+            workspace, stream, window=window, k_new=k_new, v_new=v_new, parents=parents)
 
 
 def nvfp4_lora_merge(w, lora_b, lora_a, scale: float, out, stream=None):

@@ -1,6 +1,9 @@
 // api.cu — the libnvfp4 C ABI: argument validation, device checks, the sticky
 // device status word, and dispatch to the kernels.  Every entry point is declared
 // and documented in include/nvfp4.h.
+#include <math.h>
+
+#include <initializer_list>
 #include <mutex>
 
 #include "kernels.h"
@@ -443,6 +446,132 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
                                               ot == NVFP4_BF16, ldo, status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Checks of a window's HOST lists; min_slots is 0 where the window may be empty.
+static nvfp4_status check_window(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
+                                 int32_t n_slots, int32_t min_slots, int64_t* total) {
+  if (n_slots < min_slots || n_slots > nvfp4::kMaxWindowSlots) return NVFP4_ERR_INVALID_ARG;
+  if (n_slots > 0 && (!slots_host || !tokens_host)) return NVFP4_ERR_INVALID_ARG;
+  *total = 0;
+  for (int i = 0; i < n_slots; ++i) {
+    if (slots_host[i] < 0 || slots_host[i] >= cache->max_chunks) return NVFP4_ERR_INVALID_ARG;
+    if (tokens_host[i] < 1 || tokens_host[i] > cache->chunk_tokens) return NVFP4_ERR_SHAPE;
+    *total += tokens_host[i];
+  }
+  return NVFP4_OK;
+}
+
+nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int32_t* tokens_host, int32_t n_slots,
+                                          int64_t tq, int32_t q_heads, size_t* bytes) {
+  nvfp4::KVLayout L;
+  nvfp4_status st = check_cache(cache, &L, /*needs_scratch=*/false);
+  if (st != NVFP4_OK) return st;
+  if (!bytes || (n_slots > 0 && !tokens_host)) return NVFP4_ERR_INVALID_ARG;
+  if (n_slots < 0 || n_slots > nvfp4::kMaxWindowSlots) return NVFP4_ERR_INVALID_ARG;
+  for (int i = 0; i < n_slots; ++i)
+    if (tokens_host[i] < 1 || tokens_host[i] > cache->chunk_tokens) return NVFP4_ERR_SHAPE;
+  if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0) return NVFP4_ERR_SHAPE;
+  if (tq > nvfp4::kMaxAttentionRows / (q_heads / cache->heads)) return NVFP4_ERR_SHAPE;
+  *bytes = nvfp4::attention_workspace_bytes(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
+  return NVFP4_OK;
+}
+
+// The common part of the two attention calls.  a holds what is particular to the tree.
+static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cache, const int32_t* slots_host,
+                              const int32_t* tokens_host, int32_t n_slots, const void* q, int64_t tq, int32_t q_heads,
+                              int64_t ldq, const nvfp4_attention* at, void* o_out, int64_t ldo, float* lse_out,
+                              int32_t min_slots, nvfp4_stream_t stream) {
+  nvfp4::KVLayout L;
+  nvfp4_status st = check_cache(cache, &L, /*needs_scratch=*/false);
+  if (st != NVFP4_OK) return st;
+  if (!at || at->reserved != 0 || ((!q || !o_out) && tq > 0)) return NVFP4_ERR_INVALID_ARG;
+  if (cache->head_dim != 128) return NVFP4_ERR_SHAPE;
+  int64_t total = 0;
+  if ((st = check_window(cache, slots_host, tokens_host, n_slots, min_slots, &total)) != NVFP4_OK) return st;
+  if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0 || cache->heads > 65535) return NVFP4_ERR_SHAPE;
+  if (tq > nvfp4::kMaxAttentionRows / (q_heads / cache->heads)) return NVFP4_ERR_SHAPE;
+  const int64_t width = (int64_t)q_heads * 128;
+  if (tq > 1 && (ldq < width || ldo < width)) return NVFP4_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(o_out) || (tq > 1 && ((ldq * 2) % 16 != 0 || (ldo * 2) % 16 != 0)))
+    return NVFP4_ERR_ALIGNMENT;
+  for (const void* w : {(const void*)at->slopes, (const void*)at->q_pos_dev, (const void*)at->q_doc,
+                        (const void*)at->k_doc, (const void*)lse_out})
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return NVFP4_ERR_ALIGNMENT;
+  if (!isfinite(at->scale) || !isfinite(at->softcap) || at->softcap < 0.0f) return NVFP4_ERR_INVALID_ARG;
+  if (at->causal != 0 && at->causal != 1) return NVFP4_ERR_INVALID_ARG;
+  if ((at->q_doc == nullptr) != (at->k_doc == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  constexpr int64_t kMaxPos = 0x7FFFFFFF;  // positions are int32 on the device
+  if (at->window < 0 || at->prefix < 0 || at->q_pos < 0 || at->q_pos + tq > kMaxPos) return NVFP4_ERR_SHAPE;
+  int64_t pos[nvfp4::kMaxWindowSlots];
+  int64_t next = 0;
+  for (int i = 0; i < n_slots; ++i) {
+    pos[i] = at->slot_pos_host ? at->slot_pos_host[i] : next;
+    if (pos[i] < 0 || pos[i] > kMaxPos - tokens_host[i]) return NVFP4_ERR_SHAPE;
+    next = pos[i] + tokens_host[i];
+  }
+  unsigned* status = nullptr;
+  if (tq == 0) return current_device(&status);
+  const size_t need =
+      nvfp4::attention_workspace_bytes(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
+  if (!at->workspace || at->workspace_bytes < need) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(at->workspace)) return NVFP4_ERR_ALIGNMENT;
+  if ((st = current_device(&status)) != NVFP4_OK) return st;
+  a.cache = &L;
+  a.slots = slots_host;
+  a.tokens = tokens_host;
+  a.slot_pos = pos;
+  a.n_slots = n_slots;
+  a.q = q;
+  a.tq = tq;
+  a.ldq = ldq;
+  a.q_heads = q_heads;
+  a.scale = at->scale;
+  a.cap = at->softcap;
+  a.slopes = at->slopes;
+  a.causal = at->causal != 0;
+  a.window = at->window < kMaxPos ? at->window : 0;  // as long as all positions: no limit
+  a.prefix = at->prefix < kMaxPos ? at->prefix : kMaxPos;
+  a.q_pos0 = at->q_pos;
+  a.q_pos = at->q_pos_dev;
+  a.q_doc = at->q_doc;
+  a.k_doc = at->k_doc;
+  a.o = o_out;
+  a.ldo = ldo;
+  a.lse = lse_out;
+  a.workspace = static_cast<float*>(at->workspace);
+  a.status = status;
+  return cuda_status(nvfp4::launch_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status kv_window_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
+                                 int32_t n_slots, const void* q, int64_t tq, int32_t q_heads, int64_t ldq,
+                                 const nvfp4_attention* at, void* o_out, int64_t ldo, float* lse_out,
+                                 nvfp4_stream_t stream) {
+  nvfp4::AttentionArgs a = {};
+  return attention(a, cache, slots_host, tokens_host, n_slots, q, tq, q_heads, ldq, at, o_out, ldo, lse_out, 1,
+                   stream);
+}
+
+nvfp4_status kv_tree_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
+                               int32_t n_slots, const void* q, int64_t drafts, int32_t q_heads, int64_t ldq,
+                               const void* k_new, const void* v_new, int64_t ld_new, const int32_t* parents,
+                               const nvfp4_attention* at, void* o_out, int64_t ldo, float* lse_out,
+                               nvfp4_stream_t stream) {
+  if (!cache || !at || ((!parents || !k_new || !v_new) && drafts > 0)) return NVFP4_ERR_INVALID_ARG;
+  // drafts have their places by the tree alone
+  if (at->causal || at->prefix || at->q_pos_dev || at->q_doc || at->k_doc) return NVFP4_ERR_INVALID_ARG;
+  if (drafts > nvfp4::kMaxTreeDrafts) return NVFP4_ERR_SHAPE;
+  if (drafts > 1 && ld_new < (int64_t)cache->heads * cache->head_dim) return NVFP4_ERR_SHAPE;
+  if (!aligned16(k_new) || !aligned16(v_new) || (drafts > 1 && (ld_new * 2) % 16 != 0)) return NVFP4_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(parents) & 3u) return NVFP4_ERR_ALIGNMENT;
+  nvfp4::AttentionArgs a = {};
+  a.parents = parents;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.ld_new = ld_new;
+  return attention(a, cache, slots_host, tokens_host, n_slots, q, drafts, q_heads, ldq, at, o_out, ldo, lse_out,
+                   0, stream);
+}
+
 nvfp4_status kv_dequant_window(const nvfp4_kv_cache* cache, const int32_t* slots_host,
                                int32_t n_slots, void* k_out, void* v_out, nvfp4_stream_t stream) {
   if (!cache || n_slots < 1 || n_slots > nvfp4::kMaxWindowSlots) return NVFP4_ERR_INVALID_ARG;
@@ -488,6 +617,128 @@ nvfp4_status nvfp4_amax_history_push(float* history, int32_t len, const float* a
   if (st != NVFP4_OK) return st;
   return cuda_status(nvfp4::launch_amax_history(history, len, amax_new, gscale_out, status,
                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- layer steps
+
+nvfp4_status nvfp4_rmsnorm_quantize(const void* x, int32_t xt, int64_t rows, int64_t cols, int64_t ldx,
+                                    const void* residual, int64_t ldr, const void* weight, int32_t wt, float eps,
+                                    void* h_out, int64_t ldh, const float* gscale_in, const nvfp4_tensor* out,
+                                    float* amax_out, nvfp4_stream_t stream) {
+  if ((!x && rows > 0) || !valid_dtype(xt) || (weight && !valid_dtype(wt))) return NVFP4_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || eps > 3.402823466e38f) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st = check_tensor(out);
+  if (st != NVFP4_OK) return st;
+  if (out->rows != rows || out->cols != cols) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && (ldx < cols || (residual && ldr < cols) || (h_out && ldh < cols))) return NVFP4_ERR_SHAPE;
+  if (!gscale_in && !amax_out) return NVFP4_ERR_INVALID_ARG;
+  const int64_t esz = xt == NVFP4_BF16 ? 2 : 4;
+  if (rows > 0 && (!aligned16(x) || !aligned16(residual) || !aligned16(h_out) || (ldx * esz) % 16 != 0 ||
+                   (residual && (ldr * esz) % 16 != 0) || (h_out && (ldh * esz) % 16 != 0)))
+    return NVFP4_ERR_ALIGNMENT;
+  if (!aligned16(weight) || (reinterpret_cast<uintptr_t>(amax_out) & 3u) ||
+      (reinterpret_cast<uintptr_t>(gscale_in) & 3u))
+    return NVFP4_ERR_ALIGNMENT;
+  // in place means the same buffer with the same pitch: each element is then read before it is written
+  if (rows > 0 && h_out && ((h_out == x && ldh != ldx) || (h_out == residual && ldh != ldr)))
+    return NVFP4_ERR_INVALID_ARG;
+  unsigned* status = nullptr;
+  if ((st = current_device(&status)) != NVFP4_OK) return st;
+  nvfp4::RmsnormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.h_out = h_out;
+  a.weight = weight;
+  a.x_bf16 = xt == NVFP4_BF16;
+  a.w_bf16 = wt == NVFP4_BF16;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldh = ldh;
+  a.eps = eps;
+  a.gscale_in = gscale_in;
+  a.codes = out->codes;
+  a.ld_codes = out->ld_codes;
+  a.scales = out->scales;
+  a.ld_scales = out->ld_scales;
+  a.sf_mma = out->sf_layout == NVFP4_SF_MMA;
+  a.gscale_out = out->gscale;
+  a.amax_out = amax_out;
+  a.status = status;
+  return cuda_status(nvfp4::launch_rmsnorm_quantize(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original,
+                                    double beta_fast, double beta_slow, double* freq_host, float* mscale) {
+  if (!freq_host || !mscale) return NVFP4_ERR_INVALID_ARG;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > nvfp4::kMaxRopeHeadDim) return NVFP4_ERR_SHAPE;
+  if (!(base > 1.0) || !isfinite(base)) return NVFP4_ERR_INVALID_ARG;
+  if (scaling != NVFP4_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return NVFP4_ERR_INVALID_ARG;
+  double lo = 0.0, hi = 0.0;
+  *mscale = 1.0f;
+  if (scaling == NVFP4_ROPE_BY_PARTS) {
+    if (original < 1 || !(beta_fast > beta_slow) || !(beta_slow > 0.0) || !isfinite(beta_fast))
+      return NVFP4_ERR_INVALID_ARG;
+    // the (fractional) pair that turns beta times over `original` positions
+    const double two_pi = 6.283185307179586476925;
+    lo = floor(rot_dim * log((double)original / (beta_fast * two_pi)) / (2.0 * log(base)));
+    hi = ceil(rot_dim * log((double)original / (beta_slow * two_pi)) / (2.0 * log(base)));
+    lo = lo < 0.0 ? 0.0 : lo;
+    hi = hi > rot_dim - 1 ? rot_dim - 1 : hi;
+    *mscale = (float)(0.1 * log(factor) + 1.0);
+  } else if (scaling != NVFP4_ROPE_PLAIN && scaling != NVFP4_ROPE_LINEAR) {
+    return NVFP4_ERR_INVALID_ARG;
+  }
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot_dim);
+    double stretched = 0.0;  // share of the stretched frequency
+    if (scaling == NVFP4_ROPE_LINEAR) stretched = 1.0;
+    if (scaling == NVFP4_ROPE_BY_PARTS) {
+      stretched = (i - lo) / (hi - lo > 1e-3 ? hi - lo : 1e-3);
+      stretched = stretched < 0.0 ? 0.0 : stretched > 1.0 ? 1.0 : stretched;
+    }
+    freq_host[i] = stretched == 0.0 ? f : f / factor * stretched + f * (1.0 - stretched);
+  }
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_rope(const void* x, int32_t xt, int64_t tokens, int32_t heads, int32_t head_dim, int64_t ldx,
+                        const double* freq, int32_t rot_dim, int32_t layout, float mscale, const int32_t* positions,
+                        int64_t pos0, void* y, int64_t ldy, nvfp4_stream_t stream) {
+  if (!freq || !valid_dtype(xt) || (layout != NVFP4_ROPE_HALF && layout != NVFP4_ROPE_INTERLEAVED))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((!x || !y) && tokens > 0 && heads > 0) return NVFP4_ERR_INVALID_ARG;
+  if (!isfinite(mscale)) return NVFP4_ERR_INVALID_ARG;
+  if (tokens < 0 || heads < 0 || head_dim < 2 || head_dim > nvfp4::kMaxRopeHeadDim) return NVFP4_ERR_SHAPE;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > head_dim) return NVFP4_ERR_SHAPE;
+  const int64_t width = (int64_t)heads * head_dim;
+  if (tokens > (1ll << 31) || width > (1ll << 20)) return NVFP4_ERR_SHAPE;
+  if (tokens > 1 && (ldx < width || ldy < width)) return NVFP4_ERR_SHAPE;
+  const uintptr_t esz = xt == NVFP4_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(x) % esz) || (reinterpret_cast<uintptr_t>(y) % esz) ||
+      (reinterpret_cast<uintptr_t>(freq) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return NVFP4_ERR_ALIGNMENT;
+  if (x == y && tokens > 1 && ldx != ldy) return NVFP4_ERR_INVALID_ARG;  // in place: the same layout
+  unsigned* status = nullptr;
+  nvfp4_status st = current_device(&status);
+  if (st != NVFP4_OK) return st;
+  nvfp4::RopeArgs a;
+  a.x = x;
+  a.y = y;
+  a.x_bf16 = xt == NVFP4_BF16;
+  a.interleaved = layout == NVFP4_ROPE_INTERLEAVED;
+  a.tokens = tokens;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.heads = heads;
+  a.head_dim = head_dim;
+  a.rot_dim = rot_dim;
+  a.freq = freq;
+  a.mscale = mscale;
+  a.positions = positions;
+  a.pos0 = pos0;
+  return cuda_status(nvfp4::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_debug_grid_barrier(uint32_t extra_arrivals, uint64_t wait_limit_ns) {

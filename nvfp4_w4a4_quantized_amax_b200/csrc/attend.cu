@@ -1,0 +1,575 @@
+// attend.cu — softmax attention of few query rows over a window of the NVFP4 cache, the
+// drafted tokens of a tree, and the joining of partial results (attend.cuh gives the formulas).
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace nvfp4 {
+namespace attend {
+namespace {
+
+constexpr int kRows = 16;       // query rows of a CTA: the M of one mma.sync
+constexpr int kStep = 32;       // keys a warp takes at a time
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxDrafts = kMaxTreeDrafts;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+  return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+}
+
+struct Shared {
+  SlotView view[kMaxWindowSlots];
+  float m[kWarps][kRows], l[kWarps][kRows];
+  int32_t row_pos[kRows], row_doc[kRows];
+  union {
+    float o[kWarps][kRows][kD];
+    struct {
+      int32_t parents[kMaxDrafts];
+      int16_t list[kWarps][kMaxDrafts];
+    } tree;
+  };
+};
+
+// Where row r of cache head h keeps its result: the output itself, or a partial.
+__device__ __forceinline__ void store_row(const Params& p, int part, int h, int64_t r, int d, float4 o, float log2l,
+                                          bool with_l) {
+  if (p.parts > 1) {
+    const int64_t at = ((int64_t)part * p.heads + h) * p.rows + r;
+    *reinterpret_cast<float4*>(p.part_o + at * kD + d) = o;
+    if (with_l) p.part_l[at] = log2l;
+    return;
+  }
+  const int64_t i = r / p.group;
+  const int head = h * p.group + (int)(r - i * p.group);
+  stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + d) * 2, make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)));
+  if (with_l && p.lse) p.lse[(int64_t)head * p.tq + i] = log2l * kLn2;
+}
+
+// The drafts a row sees: itself and its ancestors, one warp a row, a lane holding 4 dims, in
+// FP32.  A draft that a row does not see is never read for it, so whatever it holds (NaN, Inf)
+// cannot reach the row.
+__device__ void tree_rows(const Params& p, Shared& sh, int h, int64_t r0) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  for (int64_t r = r0 + warp; r < r0 + kRows && r < p.rows; r += kWarps) {
+    const int i = (int)(r / p.group);
+    const int head = h * p.group + (int)(r - (int64_t)i * p.group);
+    int n = 0;
+    if (lane == 0)
+      for (int j = i; j >= 0; j = parent_of(p, sh.tree.parents, j)) sh.tree.list[warp][n++] = (int16_t)j;
+    n = __shfl_sync(0xFFFFFFFFu, n, 0);
+    __syncwarp();
+    const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
+    const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
+    const float slope = p.slopes ? p.slopes[head] : 0.0f;
+    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int e0 = 0; e0 < n; e0 += 4) {
+      uint2 kw[4], vw[4];
+      float s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = e0 + e < n ? e0 + e : e0;
+        const int64_t off = (int64_t)sh.tree.list[warp][at] * p.new_pitch + ((int64_t)h * kD + 4 * lane) * 2;
+        kw[e] = *reinterpret_cast<const uint2*>(p.k_new + off);
+        vw[e] = *reinterpret_cast<const uint2*>(p.v_new + off);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
+        s[e] *= p.scale;
+        if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
+        // the list holds draft i, its parent, ...: entry e0 + e is that many positions before it
+        s[e] = (s[e] - slope * (float)(e0 + e)) * kLog2e;
+        if (e0 + e >= n || (p.window && e0 + e >= p.window)) s[e] = -INFINITY;
+      }
+      float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      if (s[0] != s[0] || s[1] != s[1] || s[2] != s[2] || s[3] != s[3]) top = NAN;
+      if (top == -INFINITY) continue;
+      top = top != top ? top : fmaxf(m, top);
+      const float a = ex2(m - top);
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (s[e] == -INFINITY) continue;
+        const float w = ex2(s[e] - top);
+        l += w;
+        o[0] = fmaf(w, bf16_lo(vw[e].x), o[0]);
+        o[1] = fmaf(w, bf16_hi(vw[e].x), o[1]);
+        o[2] = fmaf(w, bf16_lo(vw[e].y), o[2]);
+        o[3] = fmaf(w, bf16_hi(vw[e].y), o[3]);
+      }
+      m = top;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    store_row(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
+              l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
+    __syncwarp();
+  }
+}
+
+// One CTA: 16 query rows of one cache head against a range of the window's 32-key steps, the
+// steps dealt out to four warps.  mma.sync and not tcgen05: with at most 16 rows the kernel
+// waits for the cache's bytes and for their decoding, and mma.sync takes the decoded codes from
+// registers, where tcgen05 would have them stored to shared memory first.
+// Lane (g, c) = (lane / 4, lane % 4).  Scores: the contraction runs over dims in an order in
+// which lane c owns dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of key g of an
+// 8-key tile.  Values: lane (g, c) owns dims 16 g .. 16 g + 15 (8 bytes, one scale) of keys
+// 2 c, 2 c + 1 of a tile; nibbles of the two keys are interleaved before the conversion, which
+// then yields the (key, key + 1) pairs the product wants.
+template <bool kExtras>  // a cap, a bias or documents
+__global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_constant__ Params p) {
+  __shared__ Shared sh;
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int part = blockIdx.x, h = blockIdx.y;
+  const int64_t r0 = (int64_t)blockIdx.z * kRows;
+  const bool tree_part = p.parents && part == p.parts - 1;
+  const bool positions = p.causal || p.window || p.prefix || p.slopes;
+  if (p.parents && (tree_part || positions)) {
+    for (int i = threadIdx.x; i < p.drafts; i += kThreads) sh.tree.parents[i] = p.parents[i];
+    __syncthreads();
+  }
+  if (tree_part) {
+    tree_rows(p, sh, h, r0);
+    return;
+  }
+  if (threadIdx.x < kRows) {
+    const int64_t r = r0 + threadIdx.x < p.rows ? r0 + threadIdx.x : p.rows - 1;
+    const int64_t i = r / p.group;
+    int pos = p.q_pos ? p.q_pos[i] : p.q_pos0 + (int)i;
+    if (p.parents) {
+      pos = p.q_pos0;
+      if (positions)
+        for (int j = parent_of(p, sh.tree.parents, (int)i); j >= 0; j = parent_of(p, sh.tree.parents, j)) ++pos;
+    }
+    sh.row_pos[threadIdx.x] = pos;
+    if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[i] : 0;
+  }
+  const float gv_top = load_slots(p, sh.view, part == 0 && h == 0 && r0 == 0);  // synchronises the CTA
+  int q_first = sh.row_pos[0], q_last = q_first;
+#pragma unroll
+  for (int i = 1; i < kRows; ++i) {
+    q_first = min(q_first, sh.row_pos[i]);
+    q_last = max(q_last, sh.row_pos[i]);
+  }
+
+  // this lane's rows: g and g + 8; queries as binary16 A fragments and each row's factor
+  uint32_t qa[8][4];
+  float fac[2];
+  int qpos[2], qdoc[2] = {0, 0};
+  float slope[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t r = r0 + g + 8 * u;
+    const int64_t rr = r < p.rows ? r : p.rows - 1;
+    const int64_t i = rr / p.group;
+    const int head = h * p.group + (int)(rr - i * p.group);
+    const uint8_t* src = p.q + i * p.q_pitch + ((int64_t)head * kD + 32 * c) * 2;
+    uint32_t w[16];
+    unsigned top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 v = ldg_nc_v4(src + 16 * k);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+    top = max(top >> 16, top & 0xFFFFu);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // power of two that takes the row's largest element to [2^14, 2^15); a row of zeros, NaN or
+    // Inf (which then reaches the output) keeps 1, and so do exponents out of FP32's range
+    int e = 141 - (int)(top >> 7);
+    if (top == 0 || top >= 0x7F80u) e = 0;
+    e = e > 120 ? 120 : e;
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    fac[u] = p.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      qa[ks][u] = pack_f16x2(bf16_lo(w[2 * ks]) * up, bf16_hi(w[2 * ks]) * up);
+      qa[ks][2 + u] = pack_f16x2(bf16_lo(w[2 * ks + 1]) * up, bf16_hi(w[2 * ks + 1]) * up);
+    }
+    qpos[u] = sh.row_pos[g + 8 * u];
+    if (kExtras) {
+      qdoc[u] = sh.row_doc[g + 8 * u];
+      if (p.slopes) slope[u] = p.slopes[head] * kLog2e;
+    }
+  }
+
+  float o[16][4];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+  const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
+  int seg = 0, seg_at = -1;
+  float bias[2] = {0.0f, 0.0f}, mul[2] = {0.0f, 0.0f}, lg = 0.0f, inv = 1.0f;
+  int64_t key_base = 0;  // keys listed before the slot
+  bool vzero = false;
+  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  for (int st = first + warp; st < last; st += kWarps) {
+    while (st >= p.step_end[seg]) key_base += p.tokens[seg++];
+    const int t0 = (st - (seg ? p.step_end[seg - 1] : 0)) * kStep;  // first token of the step in its slot
+    const int n = min(kStep, p.tokens[seg] - t0);
+    const int kp0 = p.pos[seg] + t0;
+    if (!sh.view[seg].ok) continue;
+    int vis = visibility(p, kp0, kp0 + n - 1, q_first, q_last);
+    if (vis == 0) continue;
+    if (n < kStep || (kExtras && p.k_doc)) vis = 1;
+    if (seg != seg_at) {  // the slot's scales and q . mu of this lane's rows
+      seg_at = seg;
+      const SlotView sv = sh.view[seg];
+      lg = sv.lg, inv = sv.inv, vzero = sv.vzero;
+      const float4* mu = reinterpret_cast<const float4*>(
+          p.base + p.off_mu + (((int64_t)p.slots[seg] * p.heads + h) * kD + 32 * c) * 4);
+      float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const float4 v = __ldg(mu + ks);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x, y;
+          f16x2_to_f32x2(qa[ks][u], x, y);
+          acc[u] = fmaf(x, v.x, fmaf(y, v.y, acc[u]));
+          f16x2_to_f32x2(qa[ks][2 + u], x, y);
+          acc[u] = fmaf(x, v.z, fmaf(y, v.w, acc[u]));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float f = kExtras && p.cap > 0.0f ? fac[u] : fac[u] * kLog2e;  // log2 units without a cap
+        bias[u] = quad_sum(acc[u]) * f;
+        mul[u] = f * sv.gk;
+      }
+    }
+    const int64_t row0 = ((int64_t)t0 * p.heads + h);
+    const uint8_t* kc = p.base + p.off_k_codes + p.slots[seg] * p.slot_codes + row0 * (kD / 2);
+    const uint8_t* vc = p.base + p.off_v_codes + p.slots[seg] * p.slot_codes + row0 * (kD / 2);
+    const uint8_t* ks_ = p.base + p.off_k_scales + p.slots[seg] * p.slot_scales + row0 * (kD / 16);
+    const uint8_t* vs_ = p.base + p.off_v_scales + p.slots[seg] * p.slot_scales + row0 * (kD / 16);
+    const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
+
+    // scores of 4 tiles of 8 keys (rows behind the slot's last token repeat it and are masked)
+    float s[4][4];
+    uint4 kw[4];
+    uint32_t kb[4];
+    uint2 vw[8];
+    uint32_t vb[8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int key = min(8 * t + g, n - 1);
+      kw[t] = ldg_nc_v4(kc + key * code_step + 16 * c);
+      kb[t] = *reinterpret_cast<const uint16_t*>(ks_ + key * scale_step + 2 * c);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int key = min(8 * (t >> 1) + 2 * c + (t & 1), n - 1);
+      vw[t] = __ldg(reinterpret_cast<const uint2*>(vc + key * code_step + 8 * g));
+      vb[t] = vs_[key * scale_step + g];
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[t][k] = 0.0f;
+      const uint32_t words[4] = {kw[t].x, kw[t].y, kw[t].z, kw[t].w};
+      const uint32_t s2[2] = {e4m3_to_f16x2_bcast(kb[t] & 0xFFu), e4m3_to_f16x2_bcast(kb[t] >> 8)};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t b[4];
+        e2m1x8_times_scale(words[w], s2[w >> 1], b);
+        mma_f16(s[t], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2], qa[2 * w][3], b[0], b[1]);
+        mma_f16(s[t], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2], qa[2 * w + 1][3], b[2], b[3]);
+      }
+    }
+    // element k of a tile: row g + 8 (k / 2), key 2 c + k % 2
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int u = k >> 1, key = 8 * t + 2 * c + (k & 1);
+        float x = fmaf(s[t][k], mul[u], bias[u]);
+        if (kExtras) {
+          if (p.cap > 0.0f) x = softcap(x, p.cap, rcap) * kLog2e;
+          if (p.slopes) x = fmaf(-slope[u], fabsf((float)(qpos[u] - (kp0 + key))), x);
+        }
+        if (vis == 1) {
+          bool see = key < n && visible(p, kp0 + key, qpos[u]);
+          if (kExtras && p.k_doc) see = see && p.k_doc[key_base + t0 + min(key, n - 1)] == qdoc[u];
+          if (!see) x = -INFINITY;
+        }
+        s[t][k] = x;
+      }
+    }
+    float alpha[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) top = fmaxf(top, fmaxf(s[t][2 * u], s[t][2 * u + 1]));
+      top = quad_max(top);
+      const float mn = fmaxf(m[u], top + lg);
+      alpha[u] = mn == -INFINITY ? 1.0f : ex2(m[u] - mn);
+      m[u] = mn;
+      const float ref = mn == -INFINITY ? 0.0f : mn - lg - kShift;  // a row that has seen nothing: weights 0
+      float sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int k = 2 * u; k < 2 * u + 2; ++k) {
+          s[t][k] = ex2(s[t][k] - ref);
+          sum += s[t][k];
+        }
+      }
+      l[u] = fmaf(sum, inv, l[u] * alpha[u]);
+    }
+    if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][0] *= alpha[0];
+        o[j][1] *= alpha[0];
+        o[j][2] *= alpha[1];
+        o[j][3] *= alpha[1];
+      }
+    }
+    if (vzero) continue;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {  // 16 keys: tiles 2 ks and 2 ks + 1
+      const uint32_t a0 = pack_f16x2(s[2 * ks][0], s[2 * ks][1]), a1 = pack_f16x2(s[2 * ks][2], s[2 * ks][3]);
+      const uint32_t a2 = pack_f16x2(s[2 * ks + 1][0], s[2 * ks + 1][1]);
+      const uint32_t a3 = pack_f16x2(s[2 * ks + 1][2], s[2 * ks + 1][3]);
+      uint32_t b[2][16];  // [tile][dim of the lane's block]
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint2 wa = vw[4 * ks + 2 * t], wb = vw[4 * ks + 2 * t + 1];
+        uint32_t s2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+            : "=r"(s2)
+            : "h"((uint16_t)(vb[4 * ks + 2 * t] | (vb[4 * ks + 2 * t + 1] << 8))));
+        const uint32_t xa[2] = {wa.x, wa.y}, xb[2] = {wb.x, wb.y};
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t even[4], odd[4];
+          e2m1x8_times_scale((xa[w] & 0x0F0F0F0Fu) | ((xb[w] << 4) & 0xF0F0F0F0u), s2, even);
+          e2m1x8_times_scale(((xa[w] >> 4) & 0x0F0F0F0Fu) | (xb[w] & 0xF0F0F0F0u), s2, odd);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            b[t][8 * w + 2 * k] = even[k];
+            b[t][8 * w + 2 * k + 1] = odd[k];
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) mma_f16(o[j], a0, a1, a2, a3, b[0][j], b[1][j]);
+    }
+  }
+
+  // join the warps: element k of o[j]: row g + 8 (k / 2), dim 32 c + 16 (k % 2) + j
+  __syncthreads();  // the drafts' parents share this memory
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float ls = quad_sum(l[u]);
+    if (c == 0) {
+      sh.m[warp][g + 8 * u] = m[u];
+      sh.l[warp][g + 8 * u] = ls;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int j = 0; j < 16; j += 4)
+      *reinterpret_cast<float4*>(&sh.o[warp][g + 8 * (k >> 1)][32 * c + 16 * (k & 1) + j]) =
+          make_float4(o[j][k], o[j + 1][k], o[j + 2][k], o[j + 3][k]);
+  __syncthreads();
+  for (int r = warp; r < kRows && r0 + r < p.rows; r += kWarps) {
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (sh.l[w][r] == 0.0f) continue;  // saw nothing
+      const float f = ex2(sh.m[w][r] - top);
+      sum = fmaf(f, sh.l[w][r], sum);
+      const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][r][4 * lane]);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum * gv_top;
+    store_row(p, part, h, r0 + r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
+              sum == 0.0f ? -INFINITY : top + log2f(sum) - kShift, lane == 0);
+  }
+}
+
+// Joins the partial results: one warp a row, O = sum_i 2^(L_i - L) O_i, L = log2 sum_i 2^L_i,
+// in the order of the parts.
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Params p) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t n = (int64_t)p.heads * p.rows;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= n) return;
+  float top = -INFINITY;
+  for (int i = lane; i < p.parts; i += 32) {
+    const float l = p.part_l[i * n + row];
+    top = l != l || top != top ? NAN : fmaxf(top, l);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) {
+    const float v = __shfl_xor_sync(0xFFFFFFFFu, top, x);
+    top = v != v || top != top ? NAN : fmaxf(top, v);
+  }
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f;
+  if (top != -INFINITY) {
+    for (int i = 0; i < p.parts; ++i) {
+      const float l = p.part_l[i * n + row];
+      if (l == -INFINITY) continue;
+      const float f = ex2(l - top);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (i * n + row) * kD + 4 * lane);
+      sum += f;
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const float f = 1.0f / sum;
+    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+  }
+  const int h = (int)(row / p.rows);
+  const int64_t r = row - (int64_t)h * p.rows, i = r / p.group;
+  const int head = h * p.group + (int)(r - i * p.group);
+  stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + 4 * lane) * 2,
+         make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w)));
+  if (lane == 0 && p.lse) p.lse[(int64_t)head * p.tq + i] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------------------- host
+
+constexpr int kSms = 148;
+
+struct Plan {
+  int32_t steps, splits;
+  int64_t row_tiles;
+};
+
+// Splits the window's key steps over CTAs where rows and heads alone do not fill the GPU: about
+// three CTAs an SM, each with two steps a warp at least.
+Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+  Plan plan;
+  int64_t steps = 0;
+  for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + kStep - 1) / kStep;
+  plan.steps = (int32_t)steps;
+  plan.row_tiles = (rows + kRows - 1) / kRows;
+  const int64_t base = plan.row_tiles * heads;
+  int64_t splits = base > 0 ? 3 * kSms / base : 1;
+  splits = std::min<int64_t>(splits, steps / (2 * kWarps));
+  plan.splits = (int32_t)std::max<int64_t>(splits, 1);
+  return plan;
+}
+
+}  // namespace
+}  // namespace attend
+
+size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows);
+  return (size_t)(plan.splits + 1) * heads * rows * (attend::kD + 1) * sizeof(float);
+}
+
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+  using namespace attend;
+  if (a.tq == 0) return cudaSuccess;
+  const KVLayout& c = *a.cache;
+  Params p = {};
+  p.base = c.base;
+  p.off_k_codes = c.off_k_codes;
+  p.off_v_codes = c.off_v_codes;
+  p.off_k_scales = c.off_k_scales;
+  p.off_v_scales = c.off_v_scales;
+  p.off_mu = c.off_mu;
+  p.off_gscale = c.off_gscale;
+  p.off_tokens = c.off_tokens;
+  p.slot_codes = c.slot_codes_bytes;
+  p.slot_scales = c.slot_scales_bytes;
+  p.heads = c.heads;
+  p.group = a.q_heads / c.heads;
+  p.n_slots = a.n_slots;
+  p.rows = a.tq * p.group;
+  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows);
+  int32_t steps = 0;
+  for (int i = 0; i < a.n_slots; ++i) {
+    p.slots[i] = a.slots[i];
+    p.tokens[i] = a.tokens[i];
+    p.pos[i] = (int32_t)a.slot_pos[i];
+    steps += (a.tokens[i] + kStep - 1) / kStep;
+    p.step_end[i] = steps;
+  }
+  p.steps = plan.steps;
+  p.splits = plan.splits;
+  p.q = (const uint8_t*)a.q;
+  p.q_pitch = a.ldq * 2;
+  p.scale = a.scale;
+  p.cap = a.cap;
+  p.slopes = a.slopes;
+  p.causal = a.causal;
+  p.window = (int32_t)a.window;
+  p.prefix = (int32_t)a.prefix;
+  p.q_pos0 = (int32_t)a.q_pos0;
+  p.q_pos = a.q_pos;
+  p.q_doc = a.q_doc;
+  p.k_doc = a.k_doc;
+  p.parents = a.parents;
+  p.k_new = (const uint8_t*)a.k_new;
+  p.v_new = (const uint8_t*)a.v_new;
+  p.new_pitch = a.ld_new * 2;
+  p.drafts = a.parents ? (int32_t)a.tq : 0;
+  p.o = (uint8_t*)a.o;
+  p.o_pitch = a.ldo * 2;
+  p.lse = a.lse;
+  p.tq = a.tq;
+  p.status = a.status;
+  p.parts = plan.splits + (a.parents ? 1 : 0);
+  if (p.parts > 1) {
+    p.part_o = a.workspace;
+    p.part_l = a.workspace + (int64_t)p.parts * p.heads * p.rows * kD;
+  }
+  const dim3 grid(p.parts, p.heads, (unsigned)plan.row_tiles);
+  cudaError_t e;
+  if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_pdl(attend_rows_kernel<true>, grid, kThreads, 0, s, p);
+  else e = launch_pdl(attend_rows_kernel<false>, grid, kThreads, 0, s, p);
+  if (e != cudaSuccess || p.parts == 1) return e;
+  const int64_t n = (int64_t)p.heads * p.rows;
+  return launch_pdl(attend_join_kernel, dim3((unsigned)((n + 7) / 8)), 256, 0, s, p);
+}
+
+}  // namespace nvfp4

@@ -124,6 +124,39 @@ cudaError_t launch_kv_context(const KVLayout& c, const int32_t* slots, const int
                               const void* p, int64_t tq, int64_t ld_p, void* o_out, bool o_bf16, int64_t ldo,
                               unsigned* status, cudaStream_t s);
 
+// Softmax attention over a window, optionally with the drafted tokens of a tree behind it
+// (parents != nullptr: tq drafts).
+constexpr int kMaxTreeDrafts = 1024;
+constexpr int64_t kMaxAttentionRows = 65535 * 16;  // tq * q_heads / heads
+struct AttentionArgs {
+  const KVLayout* cache;
+  const int32_t* slots;
+  const int32_t* tokens;
+  const int64_t* slot_pos;  // position of each slot's first token
+  int32_t n_slots;
+  const void* q;  // bf16 [tq][q_heads][128], pitch ldq elements
+  int64_t tq, ldq;
+  int32_t q_heads;
+  float scale, cap;
+  const float* slopes;  // nullable [q_heads]
+  bool causal;
+  int64_t window, prefix, q_pos0;
+  const int32_t* q_pos;  // nullable [tq]
+  const int32_t* q_doc;  // nullable, with k_doc
+  const int32_t* k_doc;
+  const int32_t* parents;  // nullable [tq]
+  const void* k_new;
+  const void* v_new;
+  int64_t ld_new;
+  void* o;
+  int64_t ldo;
+  float* lse;        // nullable [q_heads][tq]
+  float* workspace;  // attention_workspace_bytes
+  unsigned* status;
+};
+size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+
 // Test hook of the grid barrier of the one-launch quantization (see
 // nvfp4_debug_grid_barrier): arrivals a barrier waits for beyond the grid's CTAs
 // (0 = none) and its time limit (0 = the default 2 s).
@@ -150,6 +183,40 @@ struct LoraArgs {
   int64_t ldo;
 };
 cudaError_t launch_lora_merge(const LoraArgs& a, cudaStream_t s);
+
+struct RmsnormArgs {
+  const void* x;         // bf16 or fp32 [rows][ldx]
+  const void* residual;  // nullable, the same type, [rows][ldr]
+  void* h_out;           // nullable, the same type, [rows][ldh]; may be x or residual
+  const void* weight;    // nullable, bf16 or fp32 [cols]
+  bool x_bf16, w_bf16;
+  int64_t rows, cols, ldx, ldr, ldh;
+  float eps;
+  const float* gscale_in;  // nullable
+  uint8_t* codes;
+  int64_t ld_codes;
+  uint8_t* scales;
+  int64_t ld_scales;
+  bool sf_mma;
+  float* gscale_out;
+  float* amax_out;  // required when gscale_in == nullptr
+  unsigned* status;
+};
+cudaError_t launch_rmsnorm_quantize(const RmsnormArgs& a, cudaStream_t s);
+
+constexpr int kMaxRopeHeadDim = 4096;
+struct RopeArgs {
+  const void* x;  // bf16 or fp32 [tokens][heads][head_dim], token pitch ldx elements
+  void* y;        // the same, token pitch ldy; may be x
+  bool x_bf16, interleaved;
+  int64_t tokens, ldx, ldy;
+  int32_t heads, head_dim, rot_dim;
+  const double* freq;  // [rot_dim / 2]
+  float mscale;
+  const int32_t* positions;  // nullable: token t is at pos0 + t
+  int64_t pos0;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 
 struct GemmOperand {
   const uint8_t* codes;

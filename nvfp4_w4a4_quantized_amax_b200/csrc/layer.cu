@@ -1,0 +1,563 @@
+// layer.cu — what a transformer layer does between the GEMMs and the KV cache: RMS norm
+// with the residual's addition and NVFP4 output, and rotary positions.  Both move each
+// element once or twice and are bound by HBM.
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCached = 4;  // 16-value blocks of a row that a thread keeps in registers
+
+__device__ __forceinline__ uint4 ldg_v4(const void* p) {  // plain load: the output may be the input's buffer
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// ------------------------------------------------------------------------ RMS norm
+//   h = RN_t(x + residual)          (t: bf16 or FP32; the residual stream, stored)
+//   r = RN(1 / sqrt(sum(h^2) / cols + eps)),  the sum, the division and the root in binary64
+//   y = RN(RN(h * r) * w)
+//   codes, scales, g = the NVFP4 quantization of y (FP32)
+// The sum is binary64 because the codes are a step function of y: with an FP32 sum the
+// last bits of r would depend on the order of the adds and elements next to an E2M1 border
+// would change code with the launch shape.
+
+enum NormMode {
+  kGiven,   // g supplied: one pass over x (and residual)
+  kAmax,    // first of two passes: h, max|y|
+  kEncode,  // second of two passes: h read again (mostly L2), r recomputed, y encoded
+};
+
+struct NormParams {
+  const uint8_t* x;
+  const uint8_t* res;  // nullable
+  uint8_t* h;          // nullable
+  const uint8_t* w;    // nullable
+  int64_t x_pitch, res_pitch, h_pitch;  // bytes
+  bool w_bf16;
+  int64_t rows, vrows;  // vrows: rows rounded up to the scale layout's tile
+  int32_t nb, vnb;      // blocks a row, and with the scale layout's padding
+  double inv_cols, eps;
+  uint8_t* codes;
+  int64_t ld_codes;
+  uint8_t* scales;
+  int64_t ld_scales, groups;
+  const float* gscale_in;
+  float* gscale_out;
+  unsigned* amax;  // nullable with a supplied scale
+  bool amax_store; // one CTA sees every row: it stores the maximum instead of accumulating it
+  unsigned* status;
+};
+
+// 16 values as loaded: 8 words of bf16 pairs or 16 FP32 words.
+template <bool kBf16>
+struct Block {
+  uint32_t w[kBf16 ? 8 : 16];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      const uint4 v = ldg_v4(p + 16 * k);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k)
+      stg_v4(p + 16 * k, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+  }
+  __device__ __forceinline__ float get(int k) const {
+    if (!kBf16) return __uint_as_float(w[k % (kBf16 ? 8 : 16)]);
+    return (k & 1) ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
+  }
+  __device__ __forceinline__ void add(const Block& o) {  // FP32 sum, rounded to the stream's type
+    if (kBf16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(get(2 * k) + o.get(2 * k), get(2 * k + 1) + o.get(2 * k + 1));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(get(k) + o.get(k));
+    }
+  }
+};
+
+template <bool kBf16, int kMode>
+__device__ __forceinline__ Block<kBf16> norm_input(const NormParams& p, int64_t row, int32_t j) {
+  const int64_t off = (int64_t)j * (kBf16 ? 32 : 64);
+  Block<kBf16> b;
+  if (kMode == kEncode && p.h) {  // written by the first pass (and it may be x or residual itself)
+    b.load(p.h + row * p.h_pitch + off);
+    return b;
+  }
+  b.load(p.x + row * p.x_pitch + off);
+  if (p.res) {
+    Block<kBf16> r;
+    r.load(p.res + row * p.res_pitch + off);
+    b.add(r);
+  }
+  return b;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ double block_squares(const Block<kBf16>& b) {
+  double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const double u = b.get(k), v = b.get(k + 1);
+    s0 = fma(u, u, s0);
+    s1 = fma(v, v, s1);
+  }
+  return s0 + s1;
+}
+
+// y of one block, and its largest magnitude's bits (a NaN or Inf gives bits >= 0x7F800000).
+template <bool kBf16>
+__device__ __forceinline__ unsigned norm_values(const NormParams& p, const Block<kBf16>& b, int32_t j, float r,
+                                                float (&y)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) y[k] = b.get(k) * r;
+  if (p.w) {
+    if (p.w_bf16) {
+      const uint8_t* src = p.w + (int64_t)j * 32;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint4 v = ldg_nc_v4_l1(src + 16 * q);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[8 * q + 2 * k] *= bf16_lo(w[k]);
+          y[8 * q + 2 * k + 1] *= bf16_hi(w[k]);
+        }
+      }
+    } else {
+      const uint8_t* src = p.w + (int64_t)j * 64;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 v = ldg_nc_v4_l1(src + 16 * q);
+        y[4 * q] *= __uint_as_float(v.x);
+        y[4 * q + 1] *= __uint_as_float(v.y);
+        y[4 * q + 2] *= __uint_as_float(v.z);
+        y[4 * q + 3] *= __uint_as_float(v.w);
+      }
+    }
+  }
+  unsigned m = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(y[k]) & 0x7FFFFFFFu);
+  return m;
+}
+
+template <bool kMma>
+__device__ __forceinline__ void norm_encode(const NormParams& p, int64_t row, int32_t j, const float (&y)[16],
+                                            unsigned amax_bits, float g, float d6, float r6) {
+  const uint32_t s = block_scale_fast(__uint_as_float(amax_bits), d6, r6);
+  const BlockEncoder enc(e4m3_to_float(s) * g);
+  float v0[8], v1[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v0[k] = y[k];
+    v1[k] = y[8 + k];
+  }
+  uint2 out;
+  out.x = enc.encode8s(v0);
+  out.y = enc.encode8s(v1);
+  stg_v2(p.codes + row * p.ld_codes + (int64_t)j * 8, out);
+  p.scales[kMma ? sf_mma_offset(row, j, p.groups) : row * p.ld_scales + j] = (uint8_t)s;
+}
+
+// kLanes threads a row: 8 (rows up to 8 blocks), 32 (up to 128 blocks), or the whole CTA.
+template <int kLanes>
+__device__ __forceinline__ double row_sum(double v, double* red, int warps) {
+#pragma unroll
+  for (int o = (kLanes == 8 ? 4 : 16); o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (kLanes <= 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  for (int w = 0; w < warps; ++w) s += red[w];  // the same order in every thread and pass
+  __syncthreads();
+  return s;
+}
+
+template <bool kBf16, bool kMma, int kMode, int kLanes>
+__global__ void __launch_bounds__(kThreads) norm_kernel(NormParams p) {
+  __shared__ double red[kThreads / 32];
+  __shared__ unsigned redm[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int lanes = kLanes > 32 ? (int)blockDim.x : kLanes;
+  const int per_cta = (int)blockDim.x / lanes, warps = (int)blockDim.x / 32;
+  const int lane = (int)threadIdx.x % lanes;
+  float g = 0.0f;
+  if (kMode == kGiven) {
+    g = *p.gscale_in;
+    if (!(g >= 0.0f) || !(g <= 3.402823466e38f)) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, kStatusNonfinite);
+      return;
+    }
+  } else if (kMode == kEncode) {
+    const unsigned ab = *p.amax;
+    if (ab >= 0x7F800000u) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, kStatusNonfinite);
+      return;
+    }
+    g = __uint_as_float(ab) / 2688.0f;
+  }
+  if (kMode != kAmax && blockIdx.x == 0 && threadIdx.x == 0) *p.gscale_out = g;
+  const float d6 = 6.0f * g, r6 = 1.0f / d6;
+  const bool encodes = kMode != kAmax;
+  const int64_t row_end = kMma && encodes ? p.vrows : p.rows;
+  unsigned local_max = 0;
+  // every thread of the CTA takes the same number of steps: the reductions are collective
+  for (int64_t base = (int64_t)blockIdx.x * per_cta; base < row_end; base += (int64_t)gridDim.x * per_cta) {
+    const int64_t row = base + threadIdx.x / lanes;
+    const bool live = row < p.rows;
+    Block<kBf16> kept[kCached];
+    double ss = 0.0;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < kCached; ++i) {
+        const int32_t j = lane + i * lanes;
+        if (j < p.nb) kept[i] = norm_input<kBf16, kMode>(p, row, j);
+      }
+#pragma unroll
+      for (int i = 0; i < kCached; ++i) {
+        const int32_t j = lane + i * lanes;
+        if (j < p.nb) {
+          if (kMode != kEncode && p.h) kept[i].store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64));
+          ss += block_squares(kept[i]);
+        }
+      }
+      for (int32_t j = lane + kCached * lanes; j < p.nb; j += lanes) {  // rows too wide for the registers
+        const Block<kBf16> b = norm_input<kBf16, kMode>(p, row, j);
+        if (kMode != kEncode && p.h) b.store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64));
+        ss += block_squares(b);
+      }
+    }
+    ss = row_sum<kLanes>(ss, red, warps);
+    const float r = (float)(1.0 / sqrt(ss * p.inv_cols + p.eps));
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < kCached; ++i) {
+        const int32_t j = lane + i * lanes;
+        if (j < p.nb) {
+          float y[16];
+          const unsigned m = norm_values(p, kept[i], j, r, y);
+          local_max = max(local_max, m);
+          if (encodes) norm_encode<kMma>(p, row, j, y, m, g, d6, r6);
+        }
+      }
+      for (int32_t j = lane + kCached * lanes; j < p.nb; j += lanes) {
+        // h_out when there is one: it may be x's or residual's buffer, which is gone by now
+        const Block<kBf16> b = norm_input<kBf16, kEncode>(p, row, j);
+        float y[16];
+        const unsigned m = norm_values(p, b, j, r, y);
+        local_max = max(local_max, m);
+        if (encodes) norm_encode<kMma>(p, row, j, y, m, g, d6, r6);
+      }
+    }
+    if (kMma && encodes && row < p.vrows)  // padding of the tensor-core scale layout
+      for (int32_t j = live ? p.nb + lane : lane; j < p.vnb; j += lanes) p.scales[sf_mma_offset(row, j, p.groups)] = 0;
+  }
+  if (kMode == kEncode) return;
+  if (local_max >= 0x7F800000u) set_status(p.status, kStatusNonfinite);
+  if (!p.amax) return;
+  local_max = warp_max_u32(local_max);
+  if ((threadIdx.x & 31) == 0) redm[threadIdx.x >> 5] = local_max;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < warps; ++w) local_max = max(local_max, redm[w]);
+    if (p.amax_store) *p.amax = local_max;
+    else if (local_max != 0u) atomicMax(p.amax, local_max);
+  }
+}
+
+template <bool kBf16, bool kMma, int kMode, int kLanes>
+cudaError_t launch_norm_kernel(const NormParams& p, int threads, cudaStream_t s) {
+  const int per_cta = kLanes > 32 ? 1 : threads / kLanes;
+  const int64_t rows = kMma && kMode != kAmax ? p.vrows : p.rows;
+  // one wave of CTAs; a row a CTA (or 8 or 32 of them) at a time
+  static std::atomic<int> resident[64][kThreads / 32 + 1];  // per device and CTA size; racing writers agree
+  int dev = 0, wave = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* known = dev >= 0 && dev < 64 ? &resident[dev][threads / 32] : nullptr;
+  if (known) wave = known->load(std::memory_order_relaxed);
+  if (wave == 0) {
+    int per_sm = 0, sms = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_kernel<kBf16, kMma, kMode, kLanes>, threads, 0);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    wave = per_sm * sms;
+    if (known) known->store(wave, std::memory_order_relaxed);
+  }
+  const int64_t want = (rows + per_cta - 1) / per_cta;
+  const int grid = (int)(want < wave ? want : wave);
+  return launch_pdl(norm_kernel<kBf16, kMma, kMode, kLanes>, grid, threads, 0, s, p);
+}
+
+template <bool kBf16, bool kMma, int kMode>
+cudaError_t launch_norm_mode(const NormParams& p, cudaStream_t s) {
+  if (p.nb <= 8) return launch_norm_kernel<kBf16, kMma, kMode, 8>(p, kThreads, s);
+  if (p.nb <= 32 * kCached) return launch_norm_kernel<kBf16, kMma, kMode, 32>(p, kThreads, s);
+  // as many threads as share the row's blocks evenly
+  const int rounds = (p.nb + kThreads - 1) / kThreads;
+  const int threads = ((p.nb + rounds - 1) / rounds + 31) / 32 * 32;
+  return launch_norm_kernel<kBf16, kMma, kMode, kThreads>(p, threads, s);
+}
+
+template <bool kBf16, bool kMma>
+cudaError_t launch_norm(NormParams& p, cudaStream_t s) {
+  if (p.gscale_in) {
+    if (p.amax) {
+      cudaError_t e = launch_zero_words(p.amax, 1, s);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_norm_mode<kBf16, kMma, kGiven>(p, s);
+  }
+  cudaError_t e = launch_zero_words(p.amax, 1, s);
+  if (e != cudaSuccess) return e;
+  e = launch_norm_mode<kBf16, kMma, kAmax>(p, s);
+  if (e != cudaSuccess) return e;
+  return launch_norm_mode<kBf16, kMma, kEncode>(p, s);
+}
+
+// ---------------------------------------------------------------- rotary positions
+//   (a, b) -> (a cos - b sin, a sin + b cos),  angle = position * frequency
+// The angle is formed in binary64 as a number of turns, so that only its fraction is left
+// for the FP32 sine and cosine (at position 10^6 an FP32 angle would be off by 2^-5).  A CTA
+// takes a few tokens, computes their cosines and sines once into shared memory and applies
+// them to its heads.
+
+struct RopeParams {
+  const uint8_t* x;
+  uint8_t* y;
+  int64_t x_pitch, y_pitch;  // bytes a token
+  int64_t tokens;
+  int32_t heads, head_bytes;
+  int32_t half;       // rot_dim / 2
+  int32_t tile;       // tokens a CTA
+  int32_t head_split; // heads a CTA
+  int32_t units;      // work items a (token, head): rotated ones first, then copied ones
+  int32_t turned;     // of these, rotated
+  FastDiv by_units, by_heads, by_last_heads;  // by_last_heads: the last CTA column may hold fewer heads
+  const double* freq;
+  float mscale;
+  const int32_t* pos;  // nullable
+  int64_t pos0;
+};
+
+// kVec elements (16 bytes) of a and of b an item, or single pairs where alignment or the
+// number of rotated elements does not allow it.
+template <bool kBf16, bool kInterleaved, bool kVector>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
+  constexpr int kEsz = kBf16 ? 2 : 4;
+  constexpr int kVec = kVector ? 16 / kEsz : 1;          // elements of one 16-byte access
+  constexpr int kPairs = kVector ? (kInterleaved ? kVec / 2 : kVec) : 1;  // pairs an item
+  extern __shared__ float2 trig[];  // [token][pair group of 2][item] (two pairs = one 16-byte read)
+  pdl_trigger();
+  pdl_wait();
+  const int64_t t0 = (int64_t)blockIdx.x * p.tile;
+  const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
+  const int h0 = blockIdx.y * p.head_split;
+  const int nh = p.heads - h0 < p.head_split ? p.heads - h0 : p.head_split;
+  for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
+    const int t = i / p.half, k = i - t * p.half;
+    const int64_t pos = p.pos ? (int64_t)p.pos[t0 + t] : p.pos0 + t0 + t;
+    double turns = (double)pos * (p.freq[k] * 0.15915494309189533577);  // 1 / (2 pi)
+    turns -= rint(turns);
+    float s, c;
+    sincospif((float)(2.0 * turns), &s, &c);
+    const int item = k / kPairs, e = k - item * kPairs;
+    const int at = kVector ? t * p.half + (e / 2) * (2 * p.turned) + item * 2 + (e & 1) : i;
+    trig[at] = make_float2(c * p.mscale, s * p.mscale);
+  }
+  __syncthreads();
+  const int n = nt * nh * p.units;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t q = p.by_units.div((uint32_t)i);
+    const int u = i - (int)q * p.units;
+    const uint32_t t = nh == p.head_split ? p.by_heads.div(q) : p.by_last_heads.div(q);
+    const int h = h0 + (int)q - (int)t * nh;
+    const uint8_t* src = p.x + (t0 + t) * p.x_pitch + (int64_t)h * p.head_bytes;
+    uint8_t* dst = p.y + (t0 + t) * p.y_pitch + (int64_t)h * p.head_bytes;
+    if (u >= p.turned) {  // elements behind the rotated ones
+      const int64_t off = (int64_t)2 * p.half * kEsz + (int64_t)(u - p.turned) * kVec * kEsz;
+      if (kVector) stg_v4(dst + off, ldg_v4(src + off));
+      else if (kBf16) *reinterpret_cast<uint16_t*>(dst + off) = *reinterpret_cast<const uint16_t*>(src + off);
+      else *reinterpret_cast<uint32_t*>(dst + off) = *reinterpret_cast<const uint32_t*>(src + off);
+      continue;
+    }
+    float a[kPairs], b[kPairs];
+    const int64_t oa = (int64_t)u * kPairs * (kInterleaved ? 2 : 1) * kEsz;
+    const int64_t ob = kInterleaved ? oa + kEsz : oa + (int64_t)p.half * kEsz;
+    if (kVector) {
+      const uint4 va = ldg_v4(src + oa);
+      const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
+      if (kInterleaved) {
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+          a[k] = kBf16 ? bf16_lo(wa[k]) : __uint_as_float(wa[(2 * k) & 3]);
+          b[k] = kBf16 ? bf16_hi(wa[k]) : __uint_as_float(wa[(2 * k + 1) & 3]);
+        }
+      } else {
+        const uint4 vb = ldg_v4(src + ob);
+        const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+          a[k] = !kBf16 ? __uint_as_float(wa[k & 3]) : (k & 1) ? bf16_hi(wa[k / 2]) : bf16_lo(wa[k / 2]);
+          b[k] = !kBf16 ? __uint_as_float(wb[k & 3]) : (k & 1) ? bf16_hi(wb[k / 2]) : bf16_lo(wb[k / 2]);
+        }
+      }
+    } else if (kBf16) {
+      a[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + oa) << 16);
+      b[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + ob) << 16);
+    } else {
+      a[0] = *reinterpret_cast<const float*>(src + oa);
+      b[0] = *reinterpret_cast<const float*>(src + ob);
+    }
+    float oa_v[kPairs], ob_v[kPairs];
+#pragma unroll
+    for (int k = 0; k < kPairs; k += 2) {
+      float2 cs[2];
+      if (kVector) {
+        const float4 v = *reinterpret_cast<const float4*>(&trig[(int)t * p.half + (k / 2) * (2 * p.turned) + u * 2]);
+        cs[0] = make_float2(v.x, v.y);
+        cs[1] = make_float2(v.z, v.w);
+      } else {
+        cs[0] = trig[(int)t * p.half + u];
+      }
+#pragma unroll
+      for (int e = 0; e < 2 && k + e < kPairs; ++e) {
+        oa_v[k + e] = fmaf(a[k + e], cs[e].x, -(b[k + e] * cs[e].y));
+        ob_v[k + e] = fmaf(a[k + e], cs[e].y, b[k + e] * cs[e].x);
+      }
+    }
+    if (kVector) {
+      uint32_t wa[4], wb[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (kInterleaved) {
+          wa[k] = kBf16 ? pack_bf16x2(oa_v[k % kPairs], ob_v[k % kPairs])
+                        : __float_as_uint((k & 1) ? ob_v[(k / 2) % kPairs] : oa_v[(k / 2) % kPairs]);
+        } else {
+          wa[k] = kBf16 ? pack_bf16x2(oa_v[(2 * k) % kPairs], oa_v[(2 * k + 1) % kPairs]) : __float_as_uint(oa_v[k % kPairs]);
+          wb[k] = kBf16 ? pack_bf16x2(ob_v[(2 * k) % kPairs], ob_v[(2 * k + 1) % kPairs]) : __float_as_uint(ob_v[k % kPairs]);
+        }
+      }
+      stg_v4(dst + oa, make_uint4(wa[0], wa[1], wa[2], wa[3]));
+      if (!kInterleaved) stg_v4(dst + ob, make_uint4(wb[0], wb[1], wb[2], wb[3]));
+    } else if (kBf16) {
+      const uint32_t v = pack_bf16x2(oa_v[0], ob_v[0]);
+      *reinterpret_cast<uint16_t*>(dst + oa) = (uint16_t)(v & 0xFFFFu);
+      *reinterpret_cast<uint16_t*>(dst + ob) = (uint16_t)(v >> 16);
+    } else {
+      *reinterpret_cast<float*>(dst + oa) = oa_v[0];
+      *reinterpret_cast<float*>(dst + ob) = ob_v[0];
+    }
+  }
+}
+
+template <bool kBf16, bool kInterleaved, bool kVector>
+cudaError_t launch_rope_kernel(RopeParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  return launch_pdl(rope_kernel<kBf16, kInterleaved, kVector>, grid, kThreads, smem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quantize(const RmsnormArgs& a, cudaStream_t s) {
+  const int64_t esz = a.x_bf16 ? 2 : 4;
+  if (a.rows == 0) {  // an empty tensor: g as supplied or 0, max|y| = 0
+    if (a.amax_out) {
+      cudaError_t e = launch_zero_words(a.amax_out, 1, s);
+      if (e != cudaSuccess) return e;
+    }
+    if (!a.gscale_in) return launch_zero_words(a.gscale_out, 1, s);
+    return cudaMemcpyAsync(a.gscale_out, a.gscale_in, sizeof(float), cudaMemcpyDeviceToDevice, s);
+  }
+  NormParams p;
+  p.x = (const uint8_t*)a.x;
+  p.res = (const uint8_t*)a.residual;
+  p.h = (uint8_t*)a.h_out;
+  p.w = (const uint8_t*)a.weight;
+  p.x_pitch = a.ldx * esz;
+  p.res_pitch = a.ldr * esz;
+  p.h_pitch = a.ldh * esz;
+  p.w_bf16 = a.w_bf16;
+  p.rows = a.rows;
+  p.nb = (int32_t)(a.cols / 16);
+  p.groups = (p.nb + 3) / 4;
+  p.vnb = a.sf_mma ? (int32_t)p.groups * 4 : p.nb;
+  p.vrows = a.sf_mma ? (a.rows + 127) / 128 * 128 : a.rows;
+  p.inv_cols = 1.0 / (double)a.cols;
+  p.eps = (double)a.eps;
+  p.codes = a.codes;
+  p.ld_codes = a.ld_codes;
+  p.scales = a.scales;
+  p.ld_scales = a.ld_scales;
+  p.gscale_in = a.gscale_in;
+  p.gscale_out = a.gscale_out;
+  p.amax = reinterpret_cast<unsigned*>(a.amax_out);
+  p.amax_store = false;
+  p.status = a.status;
+  if (a.x_bf16) return a.sf_mma ? launch_norm<true, true>(p, s) : launch_norm<true, false>(p, s);
+  return a.sf_mma ? launch_norm<false, true>(p, s) : launch_norm<false, false>(p, s);
+}
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
+  if (a.tokens == 0 || a.heads == 0) return cudaSuccess;
+  const int esz = a.x_bf16 ? 2 : 4, vec = 16 / esz;
+  const int half = a.rot_dim / 2, tail = a.head_dim - a.rot_dim;
+  const bool inplace = a.x == a.y;
+  auto multiple = [&](int64_t elements) { return elements % vec == 0; };
+  const bool vector = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 &&
+                      multiple(a.ldx) && multiple(a.ldy) && multiple(a.head_dim) && multiple(a.rot_dim) &&
+                      (a.interleaved || multiple(half));
+  RopeParams p;
+  p.x = (const uint8_t*)a.x;
+  p.y = (uint8_t*)a.y;
+  p.x_pitch = a.ldx * esz;
+  p.y_pitch = a.ldy * esz;
+  p.tokens = a.tokens;
+  p.heads = a.heads;
+  p.head_bytes = a.head_dim * esz;
+  p.half = half;
+  const int pairs = !vector ? 1 : a.interleaved ? vec / 2 : vec;
+  p.turned = half / pairs;
+  p.units = p.turned + (inplace ? 0 : tail / (vector ? vec : 1));
+  p.freq = a.freq;
+  p.mscale = a.mscale;
+  p.pos = a.positions;
+  p.pos0 = a.pos0;
+  // about 512 angles a CTA; fewer tokens, then fewer heads, until the grid has two CTAs an SM
+  int sms = 148, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int64_t tile = 512 / half > 0 ? 512 / half : 1;
+  while (tile > 1 && (a.tokens + tile - 1) / tile < 2 * sms) tile = (tile + 1) / 2;
+  int split = a.heads;
+  while (split > 1 && (a.tokens + tile - 1) / tile * ((a.heads + split - 1) / split) < 2 * sms &&
+         (int64_t)tile * split * p.units > kThreads)
+    split = (split + 1) / 2;
+  p.tile = (int32_t)tile;
+  p.head_split = split;
+  p.by_units = FastDiv((uint32_t)p.units);
+  const dim3 grid((unsigned)((a.tokens + tile - 1) / tile), (unsigned)((a.heads + split - 1) / split));
+  p.by_heads = FastDiv((uint32_t)split);
+  p.by_last_heads = FastDiv((uint32_t)(a.heads - (a.heads - 1) / split * split));
+  const size_t smem = (size_t)tile * half * sizeof(float2);
+  if (a.x_bf16) {
+    if (a.interleaved)
+      return vector ? launch_rope_kernel<true, true, true>(p, grid, smem, s) : launch_rope_kernel<true, true, false>(p, grid, smem, s);
+    return vector ? launch_rope_kernel<true, false, true>(p, grid, smem, s) : launch_rope_kernel<true, false, false>(p, grid, smem, s);
+  }
+  if (a.interleaved)
+    return vector ? launch_rope_kernel<false, true, true>(p, grid, smem, s) : launch_rope_kernel<false, true, false>(p, grid, smem, s);
+  return vector ? launch_rope_kernel<false, false, true>(p, grid, smem, s) : launch_rope_kernel<false, false, false>(p, grid, smem, s);
+}
+
+}  // namespace nvfp4

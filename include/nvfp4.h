@@ -370,10 +370,10 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
  *   lse[h, i] = ln sum_j exp(s), over the visible keys.  A query that sees no key gets
  * O = 0 and lse = -inf.  O is stored as bf16 (RNE).  Products on the tensor cores in
  * binary16 with FP32 sums: e2m1 * s is exact there, queries are scaled by a power of two
- * a row (exact for elements down to 2^-29 of the row's largest), weights are rounded to
- * 2^-12 of their value; softmax statistics and lse are FP32.  A slot whose g_V is below
- * 2^-60 of the window's largest counts as zero values.  Non-finite queries propagate
- * into their own rows.
+ * a row (exact for elements down to 2^-29 of the row's largest), weights are rounded by
+ * at most 2^-11 of their value (2^-35 of the row's largest where they are small); softmax
+ * statistics and lse are FP32.  A slot whose g_V is below 2^-60 of the window's largest
+ * counts as zero values.  Non-finite queries propagate into their own rows.
  *   scale    : finite.  softcap: 0 (none) or positive and finite.
  *   slopes   : device fp32 [q_heads], nullable.
  *   causal   : 1: a key is visible where k_pos <= q_pos;  0: everywhere.
@@ -417,7 +417,7 @@ nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int
  *              q_heads a multiple of the cache's heads (shared heads).
  *   o_out    : device bf16 [tq][q_heads][128], row pitch ldo elements.
  *   lse_out  : device fp32 [q_heads][tq], nullable.
- * Bases and pitches 16-byte aligned; head_dim 128; tq * q_heads / heads <= 65535 * 16.
+ * Bases and pitches 16-byte aligned; head_dim 128; tq * q_heads / heads <= 65535 * 128.
  * A listed slot whose recorded token count differs sets device status NVFP4_ERR_SHAPE and
  * its keys count as masked.  Errors: INVALID_ARG, SHAPE, ALIGNMENT. */
 nvfp4_status kv_window_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnvfp4.so")
-SOURCES = ["api.cu", "quant.cu", "kv.cu", "gemm.cu", "lora.cu", "scores.cu", "layer.cu", "attend.cu"]
+SOURCES = ["api.cu", "quant.cu", "kv.cu", "gemm.cu", "lora.cu", "scores.cu", "layer.cu", "attend.cu", "attend_tiles.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tc.cuh", "attend.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

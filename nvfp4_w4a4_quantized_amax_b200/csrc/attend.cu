@@ -12,7 +12,6 @@ constexpr int kRows = 16;       // query rows of a CTA: the M of one mma.sync
 constexpr int kStep = 32;       // keys a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxDrafts = kMaxTreeDrafts;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -44,92 +43,11 @@ struct Shared {
   union {
     float o[kWarps][kRows][kD];
     struct {
-      int32_t parents[kMaxDrafts];
-      int16_t list[kWarps][kMaxDrafts];
+      int32_t parents[kMaxTreeDrafts];
+      int16_t list[kWarps][kMaxTreeDrafts];
     } tree;
   };
 };
-
-// Where row r of cache head h keeps its result: the output itself, or a partial.
-__device__ __forceinline__ void store_row(const Params& p, int part, int h, int64_t r, int d, float4 o, float log2l,
-                                          bool with_l) {
-  if (p.parts > 1) {
-    const int64_t at = ((int64_t)part * p.heads + h) * p.rows + r;
-    *reinterpret_cast<float4*>(p.part_o + at * kD + d) = o;
-    if (with_l) p.part_l[at] = log2l;
-    return;
-  }
-  const int64_t i = r / p.group;
-  const int head = h * p.group + (int)(r - i * p.group);
-  stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + d) * 2, make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)));
-  if (with_l && p.lse) p.lse[(int64_t)head * p.tq + i] = log2l * kLn2;
-}
-
-// The drafts a row sees: itself and its ancestors, one warp a row, a lane holding 4 dims, in
-// FP32.  A draft that a row does not see is never read for it, so whatever it holds (NaN, Inf)
-// cannot reach the row.
-__device__ void tree_rows(const Params& p, Shared& sh, int h, int64_t r0) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-  for (int64_t r = r0 + warp; r < r0 + kRows && r < p.rows; r += kWarps) {
-    const int i = (int)(r / p.group);
-    const int head = h * p.group + (int)(r - (int64_t)i * p.group);
-    int n = 0;
-    if (lane == 0)
-      for (int j = i; j >= 0; j = parent_of(p, sh.tree.parents, j)) sh.tree.list[warp][n++] = (int16_t)j;
-    n = __shfl_sync(0xFFFFFFFFu, n, 0);
-    __syncwarp();
-    const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
-    const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-    const float slope = p.slopes ? p.slopes[head] : 0.0f;
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int e0 = 0; e0 < n; e0 += 4) {
-      uint2 kw[4], vw[4];
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = e0 + e < n ? e0 + e : e0;
-        const int64_t off = (int64_t)sh.tree.list[warp][at] * p.new_pitch + ((int64_t)h * kD + 4 * lane) * 2;
-        kw[e] = *reinterpret_cast<const uint2*>(p.k_new + off);
-        vw[e] = *reinterpret_cast<const uint2*>(p.v_new + off);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
-        s[e] *= p.scale;
-        if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
-        // the list holds draft i, its parent, ...: entry e0 + e is that many positions before it
-        s[e] = (s[e] - slope * (float)(e0 + e)) * kLog2e;
-        if (e0 + e >= n || (p.window && e0 + e >= p.window)) s[e] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-      if (s[0] != s[0] || s[1] != s[1] || s[2] != s[2] || s[3] != s[3]) top = NAN;
-      if (top == -INFINITY) continue;
-      top = top != top ? top : fmaxf(m, top);
-      const float a = ex2(m - top);
-      l *= a;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] *= a;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (s[e] == -INFINITY) continue;
-        const float w = ex2(s[e] - top);
-        l += w;
-        o[0] = fmaf(w, bf16_lo(vw[e].x), o[0]);
-        o[1] = fmaf(w, bf16_hi(vw[e].x), o[1]);
-        o[2] = fmaf(w, bf16_lo(vw[e].y), o[2]);
-        o[3] = fmaf(w, bf16_hi(vw[e].y), o[3]);
-      }
-      m = top;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    store_row(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
-              l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
-    __syncwarp();
-  }
-}
 
 // One CTA: 16 query rows of one cache head against a range of the window's 32-key steps, the
 // steps dealt out to four warps.  mma.sync and not tcgen05: with at most 16 rows the kernel
@@ -148,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int part = blockIdx.x, h = blockIdx.y;
-  const int64_t r0 = (int64_t)blockIdx.z * kRows;
+  constexpr int64_t r0 = 0;
   const bool tree_part = p.parents && part == p.parts - 1;
   const bool positions = p.causal || p.window || p.prefix || p.slopes;
   if (p.parents && (tree_part || positions)) {
@@ -156,19 +74,13 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
     __syncthreads();
   }
   if (tree_part) {
-    tree_rows(p, sh, h, r0);
+    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, r0, r0 + kRows, kWarps);
     return;
   }
   if (threadIdx.x < kRows) {
     const int64_t r = r0 + threadIdx.x < p.rows ? r0 + threadIdx.x : p.rows - 1;
     const int64_t i = r / p.group;
-    int pos = p.q_pos ? p.q_pos[i] : p.q_pos0 + (int)i;
-    if (p.parents) {
-      pos = p.q_pos0;
-      if (positions)
-        for (int j = parent_of(p, sh.tree.parents, (int)i); j >= 0; j = parent_of(p, sh.tree.parents, j)) ++pos;
-    }
-    sh.row_pos[threadIdx.x] = pos;
+    sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
     if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[i] : 0;
   }
   const float gv_top = load_slots(p, sh.view, part == 0 && h == 0 && r0 == 0);  // synchronises the CTA
@@ -479,21 +391,40 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 constexpr int kSms = 148;
 
 struct Plan {
-  int32_t steps, splits;
-  int64_t row_tiles;
+  bool tiles;           // tensor-core form for many rows, else 16-row CTAs
+  int32_t step, steps;  // keys a step, steps in the window (none straddles two slots)
+  int32_t splits;       // CTAs that share a window
 };
 
-// Splits the window's key steps over CTAs where rows and heads alone do not fill the GPU: about
-// three CTAs an SM, each with two steps a warp at least.
+// Up to 16 rows a cache head: 16-row CTAs, about three an SM, each with two steps a warp at least.
+// More: tiles of 128 rows; the keys are split where rows and heads do not fill the SMs evenly, by
+// the least of waves * (steps a CTA + a CTA's own cost), with the partial results' traffic.
 Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   Plan plan;
+  plan.tiles = rows > kRows;
+  plan.step = plan.tiles ? kTileKeys : kStep;
   int64_t steps = 0;
-  for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + kStep - 1) / kStep;
+  for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + plan.step - 1) / plan.step;
   plan.steps = (int32_t)steps;
-  plan.row_tiles = (rows + kRows - 1) / kRows;
-  const int64_t base = plan.row_tiles * heads;
-  int64_t splits = base > 0 ? 3 * kSms / base : 1;
-  splits = std::min<int64_t>(splits, steps / (2 * kWarps));
+  int64_t splits = 1;
+  if (!plan.tiles) {
+    splits = std::min<int64_t>(heads > 0 ? 3 * kSms / heads : 1, steps / (2 * kWarps));
+  } else {
+    const bool pair = rows > kTileRows;
+    const int64_t base = heads * ((rows + (pair ? 2 : 1) * kTileRows - 1) / ((pair ? 2 : 1) * kTileRows));
+    const double step_us = pair ? 1.6 : 0.8, cta_us = 6.0;
+    double best = 0.0;
+    const int64_t least = (steps + kMaxListed - 1) / kMaxListed;
+    for (int64_t n = std::max<int64_t>(least, 1); n <= std::max<int64_t>(least, std::min<int64_t>(steps / 4, kSms)); ++n) {
+      const int64_t waves = (base * n + kSms - 1) / kSms;
+      const double join_us = n > 1 ? 4.0 + 2.0 * n * heads * rows * 516 / 5e6 : 0.0;
+      const double us = waves * ((steps + n - 1) / n * step_us + cta_us) + join_us;
+      if (best == 0.0 || us < best) {
+        best = us;
+        splits = n;
+      }
+    }
+  }
   plan.splits = (int32_t)std::max<int64_t>(splits, 1);
   return plan;
 }
@@ -531,7 +462,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     p.slots[i] = a.slots[i];
     p.tokens[i] = a.tokens[i];
     p.pos[i] = (int32_t)a.slot_pos[i];
-    steps += (a.tokens[i] + kStep - 1) / kStep;
+    steps += (a.tokens[i] + plan.step - 1) / plan.step;
     p.step_end[i] = steps;
   }
   p.steps = plan.steps;
@@ -563,9 +494,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     p.part_o = a.workspace;
     p.part_l = a.workspace + (int64_t)p.parts * p.heads * p.rows * kD;
   }
-  const dim3 grid(p.parts, p.heads, (unsigned)plan.row_tiles);
+  const dim3 grid(p.parts, p.heads);
   cudaError_t e;
-  if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_pdl(attend_rows_kernel<true>, grid, kThreads, 0, s, p);
+  if (plan.tiles) e = launch_attend_tiles(p, s);
+  else if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_pdl(attend_rows_kernel<true>, grid, kThreads, 0, s, p);
   else e = launch_pdl(attend_rows_kernel<false>, grid, kThreads, 0, s, p);
   if (e != cudaSuccess || p.parts == 1) return e;
   const int64_t n = (int64_t)p.heads * p.rows;

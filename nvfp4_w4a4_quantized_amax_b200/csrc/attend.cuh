@@ -9,8 +9,8 @@
 // per (row, slot), added to the scores as q . mu, and g_K is a factor of the scores.  The
 // queries enter as binary16 after a power-of-two scaling of each row that puts its largest
 // element in [2^14, 2^15): exact for elements down to 2^-29 of it and within 2^-40 of it
-// below.  The weights enter as binary16 with their maximum near 2^14 (relative rounding
-// 2^-12, as against 2^-9 for bf16).  g_V differs from slot to slot: relative to the window's
+// below.  The weights enter as binary16 with a row's largest between 2^10 and 2^14: rounded by
+// 2^-11 of their value at most (bf16: 2^-8), or by 2^-35 of the largest where they are small.  g_V differs from slot to slot: relative to the window's
 // largest it goes into the exponent of the weights (see SlotView::lg), and O is multiplied by
 // the largest at the end.  Scores, softmax statistics and sums are FP32.
 #pragma once
@@ -146,6 +146,105 @@ __device__ __forceinline__ int parent_of(const Params& p, const int32_t* parents
   }
   return j;
 }
+
+// Where row r of cache head h keeps its result: the output itself, or a partial.  Four dims from
+// d on; log2l = log2 of the row's sum of weights.
+__device__ __forceinline__ void store_row(const Params& p, int part, int h, int64_t r, int d, float4 o, float log2l,
+                                          bool with_l) {
+  if (p.parts > 1) {
+    const int64_t at = ((int64_t)part * p.heads + h) * p.rows + r;
+    *reinterpret_cast<float4*>(p.part_o + at * kD + d) = o;
+    if (with_l) p.part_l[at] = log2l;
+    return;
+  }
+  const int64_t i = r / p.group;
+  const int head = h * p.group + (int)(r - i * p.group);
+  stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + d) * 2, make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)));
+  if (with_l && p.lse) p.lse[(int64_t)head * p.tq + i] = log2l * kLn2;
+}
+
+// Position of row r's query.
+__device__ __forceinline__ int row_position(const Params& p, const int32_t* parents, int64_t r) {
+  const int64_t i = r / p.group;
+  if (!p.parents) return p.q_pos ? p.q_pos[i] : p.q_pos0 + (int)i;
+  int pos = p.q_pos0;
+  for (int j = parent_of(p, parents, (int)i); j >= 0; j = parent_of(p, parents, j)) ++pos;
+  return pos;
+}
+
+// The drafts that rows [r0, r1) of cache head h see: themselves and their ancestors, one warp a
+// row, a lane holding 4 dims, in FP32.  A draft that a row does not see is never read for it, so
+// whatever it holds (NaN, Inf) cannot reach the row.  list: kMaxTreeDrafts entries of this warp.
+__device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parents, int16_t* list, int h, int64_t r0,
+                                          int64_t r1, int warps) {
+  const int lane = threadIdx.x & 31;
+  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  for (int64_t r = r0 + (threadIdx.x >> 5); r < r1 && r < p.rows; r += warps) {
+    const int i = (int)(r / p.group);
+    const int head = h * p.group + (int)(r - (int64_t)i * p.group);
+    int n = 0;
+    if (lane == 0)
+      for (int j = i; j >= 0; j = parent_of(p, parents, j)) list[n++] = (int16_t)j;
+    n = __shfl_sync(0xFFFFFFFFu, n, 0);
+    __syncwarp();
+    const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
+    const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
+    const float slope = p.slopes ? p.slopes[head] : 0.0f;
+    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int e0 = 0; e0 < n; e0 += 4) {
+      uint2 kw[4], vw[4];
+      float s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = e0 + e < n ? e0 + e : e0;
+        const int64_t off = (int64_t)list[at] * p.new_pitch + ((int64_t)h * kD + 4 * lane) * 2;
+        kw[e] = *reinterpret_cast<const uint2*>(p.k_new + off);
+        vw[e] = *reinterpret_cast<const uint2*>(p.v_new + off);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
+        s[e] *= p.scale;
+        if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
+        // the list holds draft i, its parent, ...: entry e0 + e is that many positions before it
+        s[e] = (s[e] - slope * (float)(e0 + e)) * kLog2e;
+        if (e0 + e >= n || (p.window && e0 + e >= p.window)) s[e] = -INFINITY;
+      }
+      float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      if (s[0] != s[0] || s[1] != s[1] || s[2] != s[2] || s[3] != s[3]) top = NAN;
+      if (top == -INFINITY) continue;
+      top = top != top ? top : fmaxf(m, top);
+      const float a = ex2(m - top);
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (s[e] == -INFINITY) continue;
+        const float w = ex2(s[e] - top);
+        l += w;
+        o[0] = fmaf(w, bf16_lo(vw[e].x), o[0]);
+        o[1] = fmaf(w, bf16_hi(vw[e].x), o[1]);
+        o[2] = fmaf(w, bf16_lo(vw[e].y), o[2]);
+        o[3] = fmaf(w, bf16_hi(vw[e].y), o[3]);
+      }
+      m = top;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    store_row(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
+              l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
+    __syncwarp();
+  }
+}
+
+// Tensor-core form for many rows (attend_tiles.cu): key steps of kTileKeys, at most kMaxListed of
+// them a CTA.
+constexpr int kTileKeys = 128;
+constexpr int kMaxListed = 2048;
+constexpr int64_t kTileRows = 128;
+cudaError_t launch_attend_tiles(const Params& p, cudaStream_t s);
 
 }  // namespace attend
 }  // namespace nvfp4

@@ -1,0 +1,710 @@
+// attend_tiles.cu — softmax attention of many query rows over a window of the NVFP4 cache, on the
+// fifth-generation tensor cores (attend.cuh gives the formulas).
+#include <atomic>
+
+#include "attend.cuh"
+#include "tc.cuh"
+
+namespace nvfp4 {
+namespace attend {
+namespace {
+
+using namespace tc;
+
+// One CTA of four warpgroups, one CTA an SM:
+//   warps 0..3, 4..7  softmax of two score tiles of 128 rows x 128 keys: thread = row
+//   warps 8..11       decode the window's K and V to binary16 e2m1 * s in shared memory
+//   warp 12           issues the tensor core's work: S = Q K~^T and O += P V~
+// Tensor memory holds two score tiles (S0, S1: 128 columns each) and two outputs (O0, O1); the
+// weights P (binary16) take the place of the scores they come from and are the A operand of the
+// second product straight from there.  While one warpgroup computes weights the tensor core works
+// on the other's tile.
+//   kPair:  256 rows; both tiles take every key step, so a decoded step feeds 256 rows.
+//   !kPair: up to 128 rows; tile t takes the key steps t, t + 2, ... and the two results are
+//           joined at the end.
+// Both operands of both products are in the 128-byte swizzle: K~ as rows of keys (K-major), V~
+// the same way, which for O += P V~ is the MN-major B operand, so one decoder writes both.
+constexpr int kThreads = 512;
+constexpr int kTileBytes = 128 * kD * 2;    // 32 KB: two 128-row x 128-byte blocks
+constexpr int kBlockBytes = 128 * 128;
+constexpr int kStages = 2;
+constexpr int kTmemCols = 512;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// Registers: the launch's 128 a thread are moved to the softmax warpgroups, which hold a row's 128
+// scores: 2 * (192 - 128) = (128 - 88) + (128 - 40).
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsDecode = 88, kRegsIssue = 40;
+static_assert(2 * kRegsSoftmax + kRegsDecode + kRegsIssue == 4 * kRegsLaunch, "the register split must balance");
+
+// The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
+// rarely rescaled; a row's largest weight is then between 2^kUp and 2^(kUp + kLazy) = 2^14.
+constexpr float kLazy = 4.0f, kUp = 10.0f;
+
+struct Control {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_ready[2], done;
+  uint32_t tmem;
+  volatile int abort;
+  int32_t listed;
+  int32_t q_first, q_last, d_first, d_last;
+  SlotView view[kMaxWindowSlots];
+  float m[128], l[128];  // of tile 1, when the two are joined
+};
+constexpr int kControlBytes = (sizeof(Control) + 127) / 128 * 128;
+
+constexpr int smem_bytes(bool pair) {
+  return 1024 + (pair ? 2 : 1) * kTileBytes + 2 * kStages * kTileBytes + kControlBytes + kMaxListed * 4;
+}
+
+__device__ __forceinline__ uint32_t idesc(bool b_mn_major) {
+  // D FP32 (bits 4..5 = 1), A and B binary16 (0), B MN-major (bit 16), N >> 3, M >> 4
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc(false)), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc(true)), "r"(accumulate)
+      : "memory");
+}
+
+// 32 columns of this thread's lane; the values may be used after ld_wait and ld_tie.
+__device__ __forceinline__ void ld_x32(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Orders the uses of r behind the wait that was issued before this.
+__device__ __forceinline__ void ld_tie(float* r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
+                      "+f"(r[i + 6]), "+f"(r[i + 7]));
+}
+__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A listed key step: its number in the CTA's range (bits 0..11), list entry of its slot (12..18),
+// and whether every row sees all of it (20).
+__device__ __forceinline__ uint32_t listed_step(int rel, int seg, bool full) {
+  return (uint32_t)rel | ((uint32_t)seg << 12) | (full ? 1u << 20 : 0u);
+}
+
+struct Step {
+  int seg, t0, n;  // slot entry, first token in the slot, tokens
+  bool full;
+};
+__device__ __forceinline__ Step read_step(const Params& p, const uint32_t* list, int i, int first) {
+  const uint32_t v = list[i];
+  Step s;
+  s.seg = (int)((v >> 12) & 0x7Fu);
+  const int st = first + (int)(v & 0xFFFu);
+  s.t0 = (st - (s.seg ? p.step_end[s.seg - 1] : 0)) * kTileKeys;
+  s.n = min(kTileKeys, p.tokens[s.seg] - s.t0);
+  s.full = (v >> 20) & 1u;
+  return s;
+}
+
+template <bool kExtras, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_constant__ Params p) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* kbuf = qbuf + (kPair ? 2 : 1) * kTileBytes;
+  uint8_t* vbuf = kbuf + kStages * kTileBytes;
+  Control& ct = *reinterpret_cast<Control*>(vbuf + kStages * kTileBytes);
+  uint32_t* list = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&ct) + kControlBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x, h = blockIdx.y;
+  const int64_t r0 = (int64_t)blockIdx.z * (kPair ? 256 : 128);
+  const int64_t r_end = min(r0 + (kPair ? 256 : 128), p.rows);
+  const bool tree_part = p.parents && part == p.parts - 1;
+  const bool positions = p.causal || p.window || p.prefix || p.slopes;
+
+  // the drafts' parents and the lists of tree_rows take the key buffers, which are free till then
+  int32_t* parents = reinterpret_cast<int32_t*>(kbuf);
+  int16_t* ancestors = reinterpret_cast<int16_t*>(kbuf + kMaxTreeDrafts * 4) + warp * kMaxTreeDrafts;
+  static_assert(kMaxTreeDrafts * (4 + 2 * (kThreads / 32)) <= kStages * kTileBytes, "lists of tree_rows");
+  pdl_wait();
+  if (p.parents && (tree_part || positions)) {
+    for (int i = threadIdx.x; i < p.drafts; i += kThreads) parents[i] = p.parents[i];
+    __syncthreads();
+  }
+  if (tree_part) {
+    tree_rows(p, parents, ancestors, h, r0, r_end, kThreads / 32);
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < kStages; ++b) {
+      mbar_init(smem_u32(&ct.k_full[b]), 4);
+      mbar_init(smem_u32(&ct.k_empty[b]), 1);
+      mbar_init(smem_u32(&ct.v_full[b]), 4);
+      mbar_init(smem_u32(&ct.v_empty[b]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&ct.s_full[t]), 1);
+      mbar_init(smem_u32(&ct.p_ready[t]), 4);
+    }
+    mbar_init(smem_u32(&ct.done), 1);
+    ct.abort = 0;
+    ct.q_first = ct.d_first = 0x7FFFFFFF;
+    ct.q_last = ct.d_last = -0x7FFFFFFF - 1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ct.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const float gv_top = load_slots(p, ct.view, part == 0 && h == 0 && blockIdx.z == 0);  // synchronises the CTA
+
+  // this thread's row (threads 0..255; the row's last for those behind the end): position,
+  // document, and the query in binary16, scaled by a power of two, into the swizzled operand tile
+  const int tile = (warp >> 2) & 1;
+  const int64_t row = r0 + (kPair ? tile * 128 : 0) + (threadIdx.x & 127);
+  const bool live = warp < 8 && row < r_end;
+  int qpos = 0, qdoc = 0;
+  float fac = 0.0f, slope = 0.0f;
+  if (warp < 8) {
+    const int64_t rr = row < r_end ? row : r_end - 1;
+    const int64_t i = rr / p.group;
+    const int head = h * p.group + (int)(rr - i * p.group);
+    if (positions) qpos = row_position(p, parents, rr);
+    if (kExtras && p.q_doc) qdoc = p.q_doc[i];
+    if (kExtras && p.slopes) slope = p.slopes[head] * kLog2e;
+    if (kPair || tile == 0) {
+      const int lo = __reduce_min_sync(0xFFFFFFFFu, qpos), hi = __reduce_max_sync(0xFFFFFFFFu, qpos);
+      const int dlo = __reduce_min_sync(0xFFFFFFFFu, qdoc), dhi = __reduce_max_sync(0xFFFFFFFFu, qdoc);
+      if (lane == 0) {
+        atomicMin(&ct.q_first, lo);
+        atomicMax(&ct.q_last, hi);
+        atomicMin(&ct.d_first, dlo);
+        atomicMax(&ct.d_last, dhi);
+      }
+    }
+    const uint8_t* src = p.q + i * p.q_pitch + (int64_t)head * kD * 2;
+    uint32_t w[64];
+    unsigned top = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint4 v = ldg_nc_v4_l1(src + 16 * k);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 64; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+    top = max(top >> 16, top & 0xFFFFu);
+    int e = 141 - (int)(top >> 7);
+    if (top == 0 || top >= 0x7F80u) e = 0;
+    e = e > 120 ? 120 : e;
+    // a negative scale goes into the queries, so that larger products are larger scores
+    const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), p.scale);
+    fac = fabsf(p.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
+    if (kPair || tile == 0) {
+      const int r = threadIdx.x & 127;
+      uint8_t* dst = qbuf + (kPair ? tile : 0) * kTileBytes + r * 128;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live)
+          v = make_uint4(pack_f16x2(bf16_lo(w[4 * k]) * up, bf16_hi(w[4 * k]) * up),
+                         pack_f16x2(bf16_lo(w[4 * k + 1]) * up, bf16_hi(w[4 * k + 1]) * up),
+                         pack_f16x2(bf16_lo(w[4 * k + 2]) * up, bf16_hi(w[4 * k + 2]) * up),
+                         pack_f16x2(bf16_lo(w[4 * k + 3]) * up, bf16_hi(w[4 * k + 3]) * up));
+        *reinterpret_cast<uint4*>(dst + (k >> 3) * kBlockBytes + (((k & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+    }
+  }
+  __syncthreads();
+
+  // the key steps of this CTA's range that some row sees, in order
+  const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
+  const int n_range = last - first;  // at most kMaxListed
+  uint8_t* flags = kbuf;             // 0 unseen, 1 partly, 2 wholly seen; the slot's entry behind
+  uint8_t* segs = kbuf + kMaxListed;
+  for (int rel = threadIdx.x; rel < n_range; rel += kThreads) {
+    const int st = first + rel;
+    int seg = 0;
+    while (st >= p.step_end[seg]) ++seg;
+    const int t0 = (st - (seg ? p.step_end[seg - 1] : 0)) * kTileKeys;
+    const int n = min(kTileKeys, p.tokens[seg] - t0);
+    int vis = ct.view[seg].ok ? visibility(p, p.pos[seg] + t0, p.pos[seg] + t0 + n - 1, ct.q_first, ct.q_last) : 0;
+    if (vis == 2 && n < kTileKeys) vis = 1;
+    flags[rel] = (uint8_t)vis;
+    segs[rel] = (uint8_t)seg;
+  }
+  __syncthreads();
+  if (kExtras && p.k_doc) {  // one warp a step: the range of its keys' documents
+    for (int rel = warp; rel < n_range; rel += kThreads / 32) {
+      if (flags[rel] == 0) continue;
+      const int seg = segs[rel];
+      int64_t base = 0;
+      for (int i = 0; i < seg; ++i) base += p.tokens[i];
+      const int t0 = (first + rel - (seg ? p.step_end[seg - 1] : 0)) * kTileKeys;
+      const int n = min(kTileKeys, p.tokens[seg] - t0);
+      int lo = 0x7FFFFFFF, hi = -0x7FFFFFFF - 1;
+      for (int k = lane; k < n; k += 32) {
+        const int d = p.k_doc[base + t0 + k];
+        lo = min(lo, d);
+        hi = max(hi, d);
+      }
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      __syncwarp();
+      if (lane == 0) {
+        if (lo > ct.d_last || hi < ct.d_first) flags[rel] = 0;
+        else if (lo != hi || ct.d_first != ct.d_last) flags[rel] = 1;
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    int n = 0;
+    for (int b = 0; b < n_range; b += 32) {
+      const int rel = b + lane;
+      const int vis = rel < n_range ? flags[rel] : 0;
+      const unsigned seen = __ballot_sync(0xFFFFFFFFu, vis != 0);
+      if (vis) list[n + __popc(seen & ((1u << lane) - 1u))] = listed_step(rel, segs[rel], vis == 2);
+      n += __popc(seen);
+    }
+    if (lane == 0) ct.listed = n;
+  }
+  fence_before();
+  __syncthreads();  // the flags' memory belongs to the decoders from here on
+  fence_after();
+  const uint32_t tmem = ct.tmem;
+  const int n = ct.listed;
+  const bool two = kPair && r_end - r0 > 128;  // the second tile has rows
+  volatile int* abort_flag = &ct.abort;
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------------- tensor core
+      bool ok = true;
+      auto wait = [&](uint64_t& bar, int phase) {
+        if (ok && !mbar_wait(smem_u32(&bar), (uint32_t)phase & 1u, abort_flag, kWaitNs)) ok = false;
+        return ok;
+      };
+      auto scores = [&](int t, int b) {  // S_t = Q_t K~_b^T
+        const uint32_t a = smem_u32(qbuf + (kPair ? t : 0) * kTileBytes), k = smem_u32(kbuf + b * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+          mma_ss(tmem + t * 128, smem_desc(a + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), kk > 0);
+        }
+        commit(smem_u32(&ct.s_full[t]));
+      };
+      auto output = [&](int t, int b, bool accumulate) {  // O_t += P_t V~_b, 16 keys an instruction
+        const uint32_t v = smem_u32(vbuf + b * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, smem_desc(v + kk * 2048, kBlockBytes, 1024, 2),
+                 accumulate || kk > 0);
+      };
+      if (kPair) {
+        for (int j = -1; j < n && n > 0; ++j) {
+          const int b = j & 1, nb = (j + 1) & 1;
+          for (int t = 0; t < (two ? 2 : 1); ++t) {
+            const bool final_tile = t == (two ? 1 : 0);
+            if (j >= 0) {
+              if (!wait(ct.p_ready[t], j) || !wait(ct.v_full[b], j >> 1)) break;
+              fence_after();
+              output(t, b, j > 0);
+              if (final_tile) commit(smem_u32(&ct.v_empty[b]));
+            }
+            if (j + 1 < n) {
+              if (!wait(ct.k_full[nb], (j + 1) >> 1)) break;
+              fence_after();
+              scores(t, nb);
+              if (final_tile) commit(smem_u32(&ct.k_empty[nb]));
+            }
+          }
+          if (!ok) break;
+        }
+      } else {
+        for (int j = -2; j < n && n > 0; ++j) {
+          const int t = j & 1;
+          if (j >= 0) {
+            if (!wait(ct.p_ready[t], j >> 1) || !wait(ct.v_full[t], j >> 1)) break;
+            fence_after();
+            output(t, t, j > 1);
+            commit(smem_u32(&ct.v_empty[t]));
+          }
+          if (j + 2 < n) {
+            if (!wait(ct.k_full[t], (j + 2) >> 1)) break;
+            fence_after();
+            scores(t, t);
+            commit(smem_u32(&ct.k_empty[t]));
+          }
+        }
+      }
+      if (!ok) {
+        set_status(p.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      commit(smem_u32(&ct.done));
+      mbar_wait_drain(smem_u32(&ct.done), 0, kWaitNs);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ decoders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    // thread: dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of keys key0 + 32 u; the
+    // lanes of a quarter warp store to 8 different 16-byte banks (4 keys x 2 chunks of one block)
+    const int c = (lane & 1) | (((lane >> 3) & 1) << 1);
+    const int key0 = ((lane >> 1) & 3) | ((lane >> 4) << 2) | ((warp & 3) << 3);
+    const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
+    struct Raw {
+      uint4 w[4];
+      uint32_t s[4];
+    };
+    auto fetch = [&](Raw& r, const Step& st, int64_t off_codes, int64_t off_scales) {
+      const int64_t slot = p.slots[st.seg];
+      const uint8_t* codes = p.base + off_codes + slot * p.slot_codes + (int64_t)h * (kD / 2) + 16 * c;
+      const uint8_t* scales = p.base + off_scales + slot * p.slot_scales + (int64_t)h * (kD / 16) + 2 * c;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // keys behind the step's last repeat it; their weights are 0
+        const int64_t key = st.t0 + min(key0 + 32 * u, st.n - 1);
+        r.w[u] = ldg_nc_v4(codes + key * code_step);
+        r.s[u] = __ldg(reinterpret_cast<const uint16_t*>(scales + key * scale_step));
+      }
+    };
+    auto decode = [&](const Raw& r, uint8_t* buf) {
+      uint8_t* dst = buf + (c >> 1) * kBlockBytes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int key = key0 + 32 * u;
+        const uint32_t words[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
+        const uint32_t s2[2] = {e4m3_to_f16x2_bcast(r.s[u] & 0xFFu), e4m3_to_f16x2_bcast(r.s[u] >> 8)};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t v[4];
+          e2m1x8_times_scale(words[w], s2[w >> 1], v);
+          st_shared_v4(smem_u32(dst + key * 128 + (((4 * (c & 1) + w) ^ (key & 7)) << 4)),
+                       make_uint4(v[0], v[1], v[2], v[3]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    Raw rk, rv;
+    Step st;
+    if (n > 0) {
+      st = read_step(p, list, 0, first);
+      fetch(rk, st, p.off_k_codes, p.off_k_scales);
+    }
+    for (int j = 0; j < n; ++j) {
+      const int b = j & 1;
+      const uint32_t parity = (((uint32_t)j >> 1) & 1u) ^ 1u;
+      fetch(rv, st, p.off_v_codes, p.off_v_scales);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.k_empty[b]), parity, abort_flag, kWaitNs))) {
+        if (lane == 0) set_status(p.status, kStatusTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      decode(rk, kbuf + b * kTileBytes);
+      if (lane == 0) mbar_arrive(smem_u32(&ct.k_full[b]));
+      if (j + 1 < n) {
+        st = read_step(p, list, j + 1, first);
+        fetch(rk, st, p.off_k_codes, p.off_k_scales);
+      }
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.v_empty[b]), parity, abort_flag, kWaitNs))) {
+        if (lane == 0) set_status(p.status, kStatusTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      decode(rv, vbuf + b * kTileBytes);
+      if (lane == 0) mbar_arrive(smem_u32(&ct.v_full[b]));
+    }
+  } else {
+    // ------------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * 128;
+    const uint8_t* qrow = qbuf + (kPair ? tile : 0) * kTileBytes + (threadIdx.x & 127) * 128;
+    const int n_mine = kPair ? (tile == 0 || two ? n : 0) : (n + 1 - tile) / 2;
+    const float rcap = kExtras && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    float mul = 0.0f, bias = 0.0f, lg = 0.0f, inv = 1.0f;
+    bool vzero = false, ok = true;
+    int seg_at = -1;
+    int64_t key_base = 0;
+    for (int i = 0; i < n_mine; ++i) {
+      const Step st = read_step(p, list, kPair ? i : 2 * i + tile, first);
+      if (st.seg != seg_at) {  // the slot's scales, and q . mu of this row
+        for (int e = seg_at < 0 ? 0 : seg_at; e < st.seg; ++e) key_base += p.tokens[e];
+        seg_at = st.seg;
+        const SlotView sv = ct.view[seg_at];
+        lg = sv.lg, inv = sv.inv, vzero = sv.vzero;
+        const float4* mu = reinterpret_cast<const float4*>(
+            p.base + p.off_mu + ((int64_t)p.slots[seg_at] * p.heads + h) * kD * 4);
+        float acc0 = 0.0f, acc1 = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * kBlockBytes +
+                                                          (((k & 7) ^ (threadIdx.x & 7)) << 4));
+          const float4 m0 = __ldg(mu + 2 * k), m1 = __ldg(mu + 2 * k + 1);
+          float x, y;
+          f16x2_to_f32x2(v.x, x, y);
+          acc0 = fmaf(x, m0.x, acc0), acc1 = fmaf(y, m0.y, acc1);
+          f16x2_to_f32x2(v.y, x, y);
+          acc0 = fmaf(x, m0.z, acc0), acc1 = fmaf(y, m0.w, acc1);
+          f16x2_to_f32x2(v.z, x, y);
+          acc0 = fmaf(x, m1.x, acc0), acc1 = fmaf(y, m1.y, acc1);
+          f16x2_to_f32x2(v.w, x, y);
+          acc0 = fmaf(x, m1.z, acc0), acc1 = fmaf(y, m1.w, acc1);
+        }
+        const float f = kExtras && p.cap > 0.0f ? fac : fac * kLog2e;  // log2 units without a cap
+        bias = (acc0 + acc1) * f;
+        mul = f * sv.gk;
+      }
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.s_full[tile]), (uint32_t)i & 1u, abort_flag, kWaitNs))) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      float s[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ld_x32(ts + 32 * k, s + 32 * k);
+      ld_wait();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ld_tie(s + 32 * k);
+      float top = -INFINITY, scale = mul, shift = bias;
+      const bool capped = kExtras && p.cap > 0.0f, biased = kExtras && p.slopes;
+      if (st.full && !capped && !biased) {
+        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+#pragma unroll
+        for (int k = 4; k < 128; k += 8) {
+          t0 = fmaxf(t0, fmaxf(s[k], s[k + 1]));
+          t1 = fmaxf(t1, fmaxf(s[k + 2], s[k + 3]));
+          if (k + 4 < 128) {
+            t2 = fmaxf(t2, fmaxf(s[k + 4], s[k + 5]));
+            t3 = fmaxf(t3, fmaxf(s[k + 6], s[k + 7]));
+          }
+        }
+        top = fmaf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), mul, bias);
+      } else {
+        // visible: keys [lo, hi) of the step, and those below pre
+        int lo = 0, hi = st.n, pre = 0;
+        const int kp0 = p.pos[st.seg] + st.t0;
+        if (!st.full) {
+          if (p.causal) hi = (int)min((int64_t)hi, (int64_t)qpos - kp0 + 1);
+          if (p.window) lo = (int)max((int64_t)0, (int64_t)qpos - kp0 - p.window + 1);
+          if (p.prefix > kp0) pre = min(p.prefix - kp0, st.n);
+        }
+#pragma unroll
+        for (int k = 0; k < 128; ++k) {
+          float x = fmaf(s[k], mul, bias);
+          if (capped) x = softcap(x, p.cap, rcap) * kLog2e;
+          if (biased) x = fmaf(-slope, fabsf((float)(qpos - kp0 - k)), x);
+          if (!st.full) {
+            bool see = k < pre || (k >= lo && k < hi);
+            if (kExtras && p.k_doc) see = see && __ldg(p.k_doc + key_base + st.t0 + min(k, st.n - 1)) == qdoc;
+            x = see ? x : -INFINITY;
+          }
+          s[k] = x;
+          top = fmaxf(top, x);
+        }
+        scale = 1.0f;
+        shift = 0.0f;
+      }
+      const float need = top + lg;
+      const bool grow = need > m + kLazy || (m == -INFINITY && need > -INFINITY);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float alpha = grow ? ex2(m - need) : 1.0f;
+        if (grow) m = need;
+        l *= alpha;
+        if (i > 0) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            float o[32];
+            ld_x32(to + 32 * k, o);
+            ld_wait();
+            ld_tie(o);
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
+            st_x32(to + 32 * k, w);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m - lg - kUp;
+      const float c0 = shift - ref;
+      float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          float* x = s + 64 * half + k;
+          fma2(x[0], x[1], x[0], x[1], scale, scale, c0, c0);
+          fma2(x[2], x[3], x[2], x[3], scale, scale, c0, c0);
+          x[0] = ex2(x[0]), x[1] = ex2(x[1]), x[2] = ex2(x[2]), x[3] = ex2(x[3]);
+          add2(sum0, sum1, sum0, sum1, x[0], x[1]);
+          add2(sum2, sum3, sum2, sum3, x[2], x[3]);
+          w[k / 2] = pack_f16x2(x[0], x[1]);
+          w[k / 2 + 1] = pack_f16x2(x[2], x[3]);
+        }
+        if (vzero) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = 0;
+        }
+        st_x32(ts + 32 * half, w);
+      }
+      l = fmaf((sum0 + sum1) + (sum2 + sum3), inv, l);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ct.p_ready[tile]));
+    }
+    if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.done), 0, abort_flag, kWaitNs))) ok = false;
+    if (!ok) {
+      if (lane == 0) set_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    fence_after();
+    {  // after a wait that gave up as well: every softmax warp meets at the barrier below
+      float other = 0.0f;  // factor of tile 1's output, when the two are joined
+      float mine = 1.0f;
+      if (!kPair) {
+        // tile 1 hands over through the decoders' buffers, 16 bytes of a row side by side with the
+        // next row's
+        float4* hand = reinterpret_cast<float4*>(kbuf);
+        if (tile == 1) {
+          ct.m[threadIdx.x & 127] = m;
+          ct.l[threadIdx.x & 127] = l;
+          if (n_mine > 0) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              float o[32];
+              ld_x32(to + 32 * k, o);
+              ld_wait();
+              ld_tie(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                hand[(8 * k + e) * 128 + (threadIdx.x & 127)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (tile == 0) {
+          const float m1 = ct.m[threadIdx.x & 127], l1 = ct.l[threadIdx.x & 127];
+          const float mt = fmaxf(m, m1);
+          if (l1 != 0.0f) {
+            other = ex2(m1 - mt);
+            mine = l != 0.0f ? ex2(m - mt) : 0.0f;
+            l = l * mine + l1 * other;
+            m = mt;
+          }
+        }
+      }
+      if (kPair || tile == 0) {
+        const float f = l == 0.0f ? 0.0f : 1.0f / l * gv_top;
+        mine *= f;
+        other *= f;
+        const float log2l = l == 0.0f ? -INFINITY : m + log2f(l) - kUp;
+        const float4* hand = reinterpret_cast<const float4*>(kbuf);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          float o[32];
+          if (n_mine > 0) {  // warp-uniform
+            ld_x32(to + 32 * k, o);
+            ld_wait();
+            ld_tie(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (l != 0.0f && n_mine > 0 && mine != 0.0f)
+              v = make_float4(o[4 * e] * mine, o[4 * e + 1] * mine, o[4 * e + 2] * mine, o[4 * e + 3] * mine);
+            if (!kPair && other != 0.0f) {
+              const float4 u = hand[(8 * k + e) * 128 + (threadIdx.x & 127)];
+              v.x = fmaf(u.x, other, v.x);
+              v.y = fmaf(u.y, other, v.y);
+              v.z = fmaf(u.z, other, v.z);
+              v.w = fmaf(u.w, other, v.w);
+            }
+            if (live) store_row(p, part, h, row, 32 * k + 4 * e, v, log2l, k == 0 && e == 0);
+          }
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+template <bool kExtras, bool kPair>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_relaxed)) {  // doing it twice is harmless
+    // the register split balances only for this launch count: with fewer the softmax warps would
+    // wait for registers that nobody releases
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, attend_tiles_kernel<kExtras, kPair>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+    e = cudaFuncSetAttribute(attend_tiles_kernel<kExtras, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes(kPair));
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  const int64_t group = (kPair ? 2 : 1) * kTileRows;
+  return launch_pdl(attend_tiles_kernel<kExtras, kPair>, dim3(p.parts, p.heads, (unsigned)((p.rows + group - 1) / group)),
+                    kThreads, smem_bytes(kPair), s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tiles(const Params& p, cudaStream_t s) {
+  const bool extras = p.cap > 0.0f || p.slopes || p.k_doc;
+  if (p.rows > kTileRows) return extras ? launch<true, true>(p, s) : launch<false, true>(p, s);
+  return extras ? launch<true, false>(p, s) : launch<false, false>(p, s);
+}
+
+}  // namespace attend
+}  // namespace nvfp4

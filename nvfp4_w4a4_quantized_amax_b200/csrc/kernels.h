@@ -127,7 +127,7 @@ cudaError_t launch_kv_context(const KVLayout& c, const int32_t* slots, const int
 // Softmax attention over a window, optionally with the drafted tokens of a tree behind it
 // (parents != nullptr: tq drafts).
 constexpr int kMaxTreeDrafts = 1024;
-constexpr int64_t kMaxAttentionRows = 65535 * 16;  // tq * q_heads / heads
+constexpr int64_t kMaxAttentionRows = 65535 * 128;  // tq * q_heads / heads
 struct AttentionArgs {
   const KVLayout* cache;
   const int32_t* slots;

@@ -46,8 +46,9 @@ def reference(q, k, v, seen, scale, cap=0.0, slopes=None, dist=None):
     """(O, lse, tolerance of O, tolerance of lse), binary64; q [tq, hq, 128], k, v [Tk, h, 128],
     seen and dist [tq, Tk].
 
-    Tolerances: the weights are rounded to binary16 (half a step: 2^-11) with an absolute floor of
-    2^-25 at a maximum of 2^14.  A score is an FP32 sum on the tensor cores of 128 products plus
+    Tolerances: the weights are rounded to binary16: half a step, 2^-11 of their value, and half the
+    smallest step, 2^-25, where they are small; a row's largest weight is at least 2^10 there, so
+    that is 2^-35 of it.  A score is an FP32 sum on the tensor cores of 128 products plus
     the mean's part; taking 2^-19 of the sum of absolute products (eight accumulations of a
     tensor-core step of 2^-22 each, and the mean's 128 additions of 2^-24 cancel less than that),
     2^-20 of the cap and 2^-22 of the biased score, it moves p by twice that, relatively.  O is
@@ -74,7 +75,7 @@ def reference(q, k, v, seen, scale, cap=0.0, slopes=None, dist=None):
         total = p.sum(-1, keepdim=True)
         p = torch.where(total > 0, p / total, 0.0)
         o[:, h] = p @ vv
-        weight = (p * (2.0 ** -11 + 2 * err[:, None])) + seen * 2.0 ** -38
+        weight = (p * (2.0 ** -11 + 2 * err[:, None])) + seen * 2.0 ** -35
         tol[:, h] = weight @ vv.abs() + 2.0 ** -8 * o[:, h].abs() + 1e-30
         tol[:, h] += 2.0 ** -8 * tol[:, h]
         lse[h] = (top + torch.log(total))[:, 0]

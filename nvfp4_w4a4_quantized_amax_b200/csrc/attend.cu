@@ -412,10 +412,10 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   } else {
     const bool pair = rows > kTileRows;
     const int64_t base = heads * ((rows + (pair ? 2 : 1) * kTileRows - 1) / ((pair ? 2 : 1) * kTileRows));
-    const double step_us = pair ? 1.6 : 0.8, cta_us = 6.0;
+    const double step_us = pair ? 0.8 : 0.4, cta_us = 6.0;
     double best = 0.0;
     const int64_t least = (steps + kMaxListed - 1) / kMaxListed;
-    for (int64_t n = std::max<int64_t>(least, 1); n <= std::max<int64_t>(least, std::min<int64_t>(steps / 4, kSms)); ++n) {
+    for (int64_t n = std::max<int64_t>(least, 1); n <= std::max<int64_t>(least, std::min<int64_t>(steps / 8, kSms)); ++n) {
       const int64_t waves = (base * n + kSms - 1) / kSms;
       const double join_us = n > 1 ? 4.0 + 2.0 * n * heads * rows * 516 / 5e6 : 0.0;
       const double us = waves * ((steps + n - 1) / n * step_us + cta_us) + join_us;

@@ -241,8 +241,8 @@ __device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parent
 
 // Tensor-core form for many rows (attend_tiles.cu): key steps of kTileKeys, at most kMaxListed of
 // them a CTA.
-constexpr int kTileKeys = 128;
-constexpr int kMaxListed = 2048;
+constexpr int kTileKeys = 64;
+constexpr int kMaxListed = 4096;
 constexpr int64_t kTileRows = 128;
 cudaError_t launch_attend_tiles(const Params& p, cudaStream_t s);
 

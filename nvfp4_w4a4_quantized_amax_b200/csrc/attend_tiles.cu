@@ -11,29 +11,31 @@ namespace {
 
 using namespace tc;
 
-// One CTA of four warpgroups, one CTA an SM:
-//   warps 0..3, 4..7  softmax of two score tiles of 128 rows x 128 keys: thread = row
+// One CTA of four warpgroups, one CTA an SM, in steps of 64 keys:
+//   warps 0..3, 4..7  softmax of two tiles of 128 rows: thread = row
 //   warps 8..11       decode the window's K and V to binary16 e2m1 * s in shared memory
-//   warp 12           issues the tensor core's work: S = Q K~^T and O += P V~
-// Tensor memory holds two score tiles (S0, S1: 128 columns each) and two outputs (O0, O1); the
+//   warps 12, 13      issue the tensor core's work of a tile each: S = Q K~^T and O += P V~
+// Tensor memory holds, for each tile, two score buffers of 64 columns and the output (128).  The
 // weights P (binary16) take the place of the scores they come from and are the A operand of the
-// second product straight from there.  While one warpgroup computes weights the tensor core works
-// on the other's tile.
-//   kPair:  256 rows; both tiles take every key step, so a decoded step feeds 256 rows.
-//   !kPair: up to 128 rows; tile t takes the key steps t, t + 2, ... and the two results are
-//           joined at the end.
+// second product straight from there.  With two buffers the scores of the next step are ready
+// when a softmax warpgroup has finished one: with one buffer of 128 keys a tile the chain scores,
+// softmax, output ran in turn and the tensor core idled two thirds of the time.
+//   kPair:  256 rows; both tiles take every step, so a decoded step feeds 256 rows.
+//   !kPair: up to 128 rows; tile t takes the steps t, t + 2, ... and the two results are joined at
+//           the end.
 // Both operands of both products are in the 128-byte swizzle: K~ as rows of keys (K-major), V~
 // the same way, which for O += P V~ is the MN-major B operand, so one decoder writes both.
 constexpr int kThreads = 512;
-constexpr int kTileBytes = 128 * kD * 2;    // 32 KB: two 128-row x 128-byte blocks
-constexpr int kBlockBytes = 128 * 128;
-constexpr int kStages = 2;
+constexpr int kQBytes = 128 * kD * 2;        // 32 KB: two 128-row x 128-byte blocks
+constexpr int kQBlock = 128 * 128;
+constexpr int kKvBytes = kTileKeys * kD * 2;  // 16 KB: two 64-row x 128-byte blocks
+constexpr int kKvBlock = kTileKeys * 128;
+constexpr int kStages = 4;
 constexpr int kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// Registers: the launch's 128 a thread are moved to the softmax warpgroups, which hold a row's 128
-// scores: 2 * (192 - 128) = (128 - 88) + (128 - 40).
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsDecode = 88, kRegsIssue = 40;
+// Registers: the launch's 128 a thread are moved between the warpgroups.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 168, kRegsDecode = 104, kRegsIssue = 72;
 static_assert(2 * kRegsSoftmax + kRegsDecode + kRegsIssue == 4 * kRegsLaunch, "the register split must balance");
 
 // The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
@@ -42,7 +44,7 @@ constexpr float kLazy = 4.0f, kUp = 10.0f;
 
 struct Control {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_ready[2], done;
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2], done[2];  // [tile][buffer]
   uint32_t tmem;
   volatile int abort;
   int32_t listed;
@@ -53,26 +55,31 @@ struct Control {
 constexpr int kControlBytes = (sizeof(Control) + 127) / 128 * 128;
 
 constexpr int smem_bytes(bool pair) {
-  return 1024 + (pair ? 2 : 1) * kTileBytes + 2 * kStages * kTileBytes + kControlBytes + kMaxListed * 4;
+  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 4;
 }
 
-__device__ __forceinline__ uint32_t idesc(bool b_mn_major) {
-  // D FP32 (bits 4..5 = 1), A and B binary16 (0), B MN-major (bit 16), N >> 3, M >> 4
-  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-}
+// Instruction descriptor: D FP32 (bits 4..5 = 1), A and B binary16 (0), N >> 3, M >> 4; bit 16: B
+// is MN-major.
+constexpr uint32_t kIdescScores = (1u << 4) | ((uint32_t)(kTileKeys >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescOutput = (1u << 4) | (1u << 16) | ((uint32_t)(kD >> 3) << 17) | ((128u >> 4) << 24);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+// Operand descriptors as two words, so that stepping through a tile is one 32-bit addition (the
+// address field is the low word's): one thread issues every instruction of its tile.
+__device__ __forceinline__ uint64_t descriptor(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+// accumulate == false: D = A B, else D += A B
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc(false)), "r"(accumulate)
+      "l"(a), "l"(b), "r"(kIdescScores), "r"((uint32_t)accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc(true)), "r"(accumulate)
+      "r"(a), "l"(b), "r"(kIdescOutput), "r"((uint32_t)accumulate)
       : "memory");
 }
 
@@ -96,15 +103,25 @@ __device__ __forceinline__ void ld_tie(float* r) {
     asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
                       "+f"(r[i + 6]), "+f"(r[i + 7]));
 }
-__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void ld_x16(uint32_t taddr, float* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_tie16(float* r) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
+                      "+f"(r[i + 6]), "+f"(r[i + 7]));
+}
+__device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -142,9 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;
-  uint8_t* kbuf = qbuf + (kPair ? 2 : 1) * kTileBytes;
-  uint8_t* vbuf = kbuf + kStages * kTileBytes;
-  Control& ct = *reinterpret_cast<Control*>(vbuf + kStages * kTileBytes);
+  uint8_t* kbuf = qbuf + (kPair ? 2 : 1) * kQBytes;
+  uint8_t* vbuf = kbuf + kStages * kKvBytes;
+  Control& ct = *reinterpret_cast<Control*>(vbuf + kStages * kKvBytes);
   uint32_t* list = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&ct) + kControlBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x, h = blockIdx.y;
@@ -156,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   // the drafts' parents and the lists of tree_rows take the key buffers, which are free till then
   int32_t* parents = reinterpret_cast<int32_t*>(kbuf);
   int16_t* ancestors = reinterpret_cast<int16_t*>(kbuf + kMaxTreeDrafts * 4) + warp * kMaxTreeDrafts;
-  static_assert(kMaxTreeDrafts * (4 + 2 * (kThreads / 32)) <= kStages * kTileBytes, "lists of tree_rows");
+  static_assert(kMaxTreeDrafts * (4 + 2 * (kThreads / 32)) <= kStages * kKvBytes, "lists of tree_rows");
   pdl_wait();
   if (p.parents && (tree_part || positions)) {
     for (int i = threadIdx.x; i < p.drafts; i += kThreads) parents[i] = p.parents[i];
@@ -167,18 +184,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     return;
   }
 
+  const bool two = kPair && r_end - r0 > 128;  // the second tile of a pair has rows
   if (threadIdx.x == 0) {
     for (int b = 0; b < kStages; ++b) {
       mbar_init(smem_u32(&ct.k_full[b]), 4);
-      mbar_init(smem_u32(&ct.k_empty[b]), 1);
+      mbar_init(smem_u32(&ct.k_empty[b]), two ? 2 : 1);  // tiles that take a step
       mbar_init(smem_u32(&ct.v_full[b]), 4);
-      mbar_init(smem_u32(&ct.v_empty[b]), 1);
+      mbar_init(smem_u32(&ct.v_empty[b]), two ? 2 : 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&ct.s_full[t]), 1);
-      mbar_init(smem_u32(&ct.p_ready[t]), 4);
+      mbar_init(smem_u32(&ct.s_full[t][0]), 1);
+      mbar_init(smem_u32(&ct.s_full[t][1]), 1);
+      mbar_init(smem_u32(&ct.o_done[t]), 1);
+      mbar_init(smem_u32(&ct.p_ready[t][0]), 4);
+      mbar_init(smem_u32(&ct.p_ready[t][1]), 4);
+      mbar_init(smem_u32(&ct.done[t]), 1);
     }
-    mbar_init(smem_u32(&ct.done), 1);
     ct.abort = 0;
     ct.q_first = ct.d_first = 0x7FFFFFFF;
     ct.q_last = ct.d_last = -0x7FFFFFFF - 1;
@@ -217,15 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       }
     }
     const uint8_t* src = p.q + i * p.q_pitch + (int64_t)head * kD * 2;
-    uint32_t w[64];
     unsigned top = 0;
-#pragma unroll
+#pragma unroll 8
     for (int k = 0; k < 16; ++k) {
       const uint4 v = ldg_nc_v4_l1(src + 16 * k);
-      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                   __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
     }
-#pragma unroll
-    for (int k = 0; k < 64; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
     top = max(top >> 16, top & 0xFFFFu);
     int e = 141 - (int)(top >> 7);
     if (top == 0 || top >= 0x7F80u) e = 0;
@@ -235,16 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     fac = fabsf(p.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
     if (kPair || tile == 0) {
       const int r = threadIdx.x & 127;
-      uint8_t* dst = qbuf + (kPair ? tile : 0) * kTileBytes + r * 128;
-#pragma unroll
+      uint8_t* dst = qbuf + (kPair ? tile : 0) * kQBytes + r * 128;
+#pragma unroll 8
       for (int k = 0; k < 16; ++k) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (live)
-          v = make_uint4(pack_f16x2(bf16_lo(w[4 * k]) * up, bf16_hi(w[4 * k]) * up),
-                         pack_f16x2(bf16_lo(w[4 * k + 1]) * up, bf16_hi(w[4 * k + 1]) * up),
-                         pack_f16x2(bf16_lo(w[4 * k + 2]) * up, bf16_hi(w[4 * k + 2]) * up),
-                         pack_f16x2(bf16_lo(w[4 * k + 3]) * up, bf16_hi(w[4 * k + 3]) * up));
-        *reinterpret_cast<uint4*>(dst + (k >> 3) * kBlockBytes + (((k & 7) ^ (r & 7)) << 4)) = v;
+        if (live) {
+          v = ldg_nc_v4_l1(src + 16 * k);
+          v = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                         pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+        }
+        *reinterpret_cast<uint4*>(dst + (k >> 3) * kQBlock + (((k & 7) ^ (r & 7)) << 4)) = v;
       }
       fence_proxy_async_smem();
     }
@@ -308,77 +327,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   fence_after();
   const uint32_t tmem = ct.tmem;
   const int n = ct.listed;
-  const bool two = kPair && r_end - r0 > 128;  // the second tile has rows
   volatile int* abort_flag = &ct.abort;
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 12 && lane == 0) {
-      // ---------------------------------------------------------------- tensor core
+    const int t = warp - 12;
+    if (t < (two || !kPair ? 2 : 1) && lane == 0) {
+      // ---------------------------------------------------- tensor core, tile t
       bool ok = true;
       auto wait = [&](uint64_t& bar, int phase) {
         if (ok && !mbar_wait(smem_u32(&bar), (uint32_t)phase & 1u, abort_flag, kWaitNs)) ok = false;
         return ok;
       };
-      auto scores = [&](int t, int b) {  // S_t = Q_t K~_b^T
-        const uint32_t a = smem_u32(qbuf + (kPair ? t : 0) * kTileBytes), k = smem_u32(kbuf + b * kTileBytes);
+      const uint32_t hi = (uint32_t)(smem_desc(0, 0, 1024, 2) >> 32);
+      const uint32_t q_lo = (uint32_t)smem_desc(smem_u32(qbuf + (kPair ? t : 0) * kQBytes), 16, 1024, 2);
+      const uint32_t k_lo = (uint32_t)smem_desc(smem_u32(kbuf), 16, 1024, 2);
+      const uint32_t v_lo = (uint32_t)smem_desc(smem_u32(vbuf), kKvBlock, 1024, 2);
+      const uint32_t ts = tmem + t * 128, to = tmem + 256 + t * 128;
+      // a pair's tiles both take every step; else tile t takes steps t, t + 2, ...
+      const int n_mine = kPair ? n : (n + 1 - t) / 2;
+      auto scores = [&](int i) {  // S_t = Q_t K~^T of this tile's step i, 16 dims an instruction
+        const int step = kPair ? i : 2 * i + t, b = step % kStages;
+        if (!wait(ct.k_full[b], step / kStages)) return;
+        fence_after();
+        const uint32_t k = k_lo + b * (kKvBytes >> 4), d = ts + (i & 1) * kTileKeys;
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
-          mma_ss(tmem + t * 128, smem_desc(a + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), kk > 0);
-        }
-        commit(smem_u32(&ct.s_full[t]));
+        for (int kk = 0; kk < kD / 16; ++kk)
+          mma_ss(d, descriptor(q_lo + (((kk >> 2) * kQBlock + (kk & 3) * 32) >> 4), hi),
+                 descriptor(k + (((kk >> 2) * kKvBlock + (kk & 3) * 32) >> 4), hi), kk > 0);
+        commit(smem_u32(&ct.s_full[t][i & 1]));
+        commit(smem_u32(&ct.k_empty[b]));
       };
-      auto output = [&](int t, int b, bool accumulate) {  // O_t += P_t V~_b, 16 keys an instruction
-        const uint32_t v = smem_u32(vbuf + b * kTileBytes);
+      for (int i = 0; i < 2 && i < n_mine; ++i) scores(i);
+      for (int i = 0; i < n_mine && ok; ++i) {  // O_t += P_t V~, 16 keys an instruction
+        const int step = kPair ? i : 2 * i + t, b = step % kStages;
+        if (!wait(ct.v_full[b], step / kStages) || !wait(ct.p_ready[t][i & 1], i >> 1)) break;
+        fence_after();
+        const uint32_t v = v_lo + b * (kKvBytes >> 4), a = ts + (i & 1) * kTileKeys;
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, smem_desc(v + kk * 2048, kBlockBytes, 1024, 2),
-                 accumulate || kk > 0);
-      };
-      if (kPair) {
-        for (int j = -1; j < n && n > 0; ++j) {
-          const int b = j & 1, nb = (j + 1) & 1;
-          for (int t = 0; t < (two ? 2 : 1); ++t) {
-            const bool final_tile = t == (two ? 1 : 0);
-            if (j >= 0) {
-              if (!wait(ct.p_ready[t], j) || !wait(ct.v_full[b], j >> 1)) break;
-              fence_after();
-              output(t, b, j > 0);
-              if (final_tile) commit(smem_u32(&ct.v_empty[b]));
-            }
-            if (j + 1 < n) {
-              if (!wait(ct.k_full[nb], (j + 1) >> 1)) break;
-              fence_after();
-              scores(t, nb);
-              if (final_tile) commit(smem_u32(&ct.k_empty[nb]));
-            }
-          }
-          if (!ok) break;
-        }
-      } else {
-        for (int j = -2; j < n && n > 0; ++j) {
-          const int t = j & 1;
-          if (j >= 0) {
-            if (!wait(ct.p_ready[t], j >> 1) || !wait(ct.v_full[t], j >> 1)) break;
-            fence_after();
-            output(t, t, j > 1);
-            commit(smem_u32(&ct.v_empty[t]));
-          }
-          if (j + 2 < n) {
-            if (!wait(ct.k_full[t], (j + 2) >> 1)) break;
-            fence_after();
-            scores(t, t);
-            commit(smem_u32(&ct.k_empty[t]));
-          }
-        }
+          mma_ts(to, a + kk * 8, descriptor(v + kk * (2048 >> 4), hi), i > 0 || kk > 0);
+        commit(smem_u32(&ct.o_done[t]));
+        commit(smem_u32(&ct.v_empty[b]));
+        // the next scores take the buffer whose weights this reads; the two products differ in shape,
+        // so only completion orders them (the scores of step i + 1 are there already)
+        if (i + 2 < n_mine && wait(ct.o_done[t], i)) scores(i + 2);
       }
       if (!ok) {
         set_status(p.status, kStatusTimeout);
         *abort_flag = 1;
       }
-      commit(smem_u32(&ct.done));
-      mbar_wait_drain(smem_u32(&ct.done), 0, kWaitNs);
+      commit(smem_u32(&ct.done[t]));
+      mbar_wait_drain(smem_u32(&ct.done[t]), 0, kWaitNs);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
@@ -389,75 +389,81 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     const int key0 = ((lane >> 1) & 3) | ((lane >> 4) << 2) | ((warp & 3) << 3);
     const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
     struct Raw {
-      uint4 w[4];
-      uint32_t s[4];
+      uint4 w[2];
+      uint32_t s[2];
     };
     auto fetch = [&](Raw& r, const Step& st, int64_t off_codes, int64_t off_scales) {
       const int64_t slot = p.slots[st.seg];
       const uint8_t* codes = p.base + off_codes + slot * p.slot_codes + (int64_t)h * (kD / 2) + 16 * c;
       const uint8_t* scales = p.base + off_scales + slot * p.slot_scales + (int64_t)h * (kD / 16) + 2 * c;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {  // keys behind the step's last repeat it; their weights are 0
+      for (int u = 0; u < 2; ++u) {  // keys behind the step's last repeat it; their weights are 0
         const int64_t key = st.t0 + min(key0 + 32 * u, st.n - 1);
         r.w[u] = ldg_nc_v4(codes + key * code_step);
-        r.s[u] = __ldg(reinterpret_cast<const uint16_t*>(scales + key * scale_step));
+        r.s[u] = ldg_nc_u16(scales + key * scale_step);
       }
     };
-    auto decode = [&](const Raw& r, uint8_t* buf) {
-      uint8_t* dst = buf + (c >> 1) * kBlockBytes;
+    const uint32_t dst0 = (c >> 1) * kKvBlock + key0 * 128;
+    const uint32_t kdst = smem_u32(kbuf) + dst0, vdst = smem_u32(vbuf) + dst0;
+    auto decode = [&](const Raw& r, uint32_t dst) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int key = key0 + 32 * u;
+      for (int u = 0; u < 2; ++u) {
         const uint32_t words[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
         const uint32_t s2[2] = {e4m3_to_f16x2_bcast(r.s[u] & 0xFFu), e4m3_to_f16x2_bcast(r.s[u] >> 8)};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t v[4];
           e2m1x8_times_scale(words[w], s2[w >> 1], v);
-          st_shared_v4(smem_u32(dst + key * 128 + (((4 * (c & 1) + w) ^ (key & 7)) << 4)),
+          st_shared_v4(dst + u * (32 * 128) + (((4 * (c & 1) + w) ^ (key0 & 7)) << 4),
                        make_uint4(v[0], v[1], v[2], v[3]));
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
     };
-    Raw rk, rv;
-    Step st;
-    if (n > 0) {
-      st = read_step(p, list, 0, first);
-      fetch(rk, st, p.off_k_codes, p.off_k_scales);
+    // two steps' K and V on their way while one is decoded
+    Raw rk[2], rv[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (e < n) {
+        const Step st = read_step(p, list, e, first);
+        fetch(rk[e], st, p.off_k_codes, p.off_k_scales);
+        fetch(rv[e], st, p.off_v_codes, p.off_v_scales);
+      }
     }
-    for (int j = 0; j < n; ++j) {
-      const int b = j & 1;
-      const uint32_t parity = (((uint32_t)j >> 1) & 1u) ^ 1u;
-      fetch(rv, st, p.off_v_codes, p.off_v_scales);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.k_empty[b]), parity, abort_flag, kWaitNs))) {
-        if (lane == 0) set_status(p.status, kStatusTimeout);
-        *abort_flag = 1;
-        break;
+    bool ok = true;
+    for (int j0 = 0; j0 < n && ok; j0 += 2) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = j0 + e;
+        if (j >= n || !ok) break;
+        const int b = j % kStages;
+        const uint32_t parity = ((uint32_t)(j / kStages) & 1u) ^ 1u;
+        Step st;
+        if (j + 2 < n) st = read_step(p, list, j + 2, first);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.k_empty[b]), parity, abort_flag, kWaitNs));
+        if (!ok) break;
+        decode(rk[e], kdst + b * kKvBytes);
+        if (lane == 0) mbar_arrive(smem_u32(&ct.k_full[b]));
+        if (j + 2 < n) fetch(rk[e], st, p.off_k_codes, p.off_k_scales);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.v_empty[b]), parity, abort_flag, kWaitNs));
+        if (!ok) break;
+        decode(rv[e], vdst + b * kKvBytes);
+        if (lane == 0) mbar_arrive(smem_u32(&ct.v_full[b]));
+        if (j + 2 < n) fetch(rv[e], st, p.off_v_codes, p.off_v_scales);
       }
-      decode(rk, kbuf + b * kTileBytes);
-      if (lane == 0) mbar_arrive(smem_u32(&ct.k_full[b]));
-      if (j + 1 < n) {
-        st = read_step(p, list, j + 1, first);
-        fetch(rk, st, p.off_k_codes, p.off_k_scales);
-      }
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.v_empty[b]), parity, abort_flag, kWaitNs))) {
-        if (lane == 0) set_status(p.status, kStatusTimeout);
-        *abort_flag = 1;
-        break;
-      }
-      decode(rv, vbuf + b * kTileBytes);
-      if (lane == 0) mbar_arrive(smem_u32(&ct.v_full[b]));
+    }
+    if (!ok) {
+      if (lane == 0) set_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
     }
   } else {
     // ------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * 128;
-    const uint8_t* qrow = qbuf + (kPair ? tile : 0) * kTileBytes + (threadIdx.x & 127) * 128;
+    const uint8_t* qrow = qbuf + (kPair ? tile : 0) * kQBytes + (threadIdx.x & 127) * 128;
     const int n_mine = kPair ? (tile == 0 || two ? n : 0) : (n + 1 - tile) / 2;
-    const float rcap = kExtras && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     float m = -INFINITY, l = 0.0f;
     float mul = 0.0f, bias = 0.0f, lg = 0.0f, inv = 1.0f;
     bool vzero = false, ok = true;
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         float acc0 = 0.0f, acc1 = 0.0f;
 #pragma unroll 4
         for (int k = 0; k < 16; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * kBlockBytes +
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * kQBlock +
                                                           (((k & 7) ^ (threadIdx.x & 7)) << 4));
           const float4 m0 = __ldg(mu + 2 * k), m1 = __ldg(mu + 2 * k + 1);
           float x, y;
@@ -492,53 +498,72 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         bias = (acc0 + acc1) * f;
         mul = f * sv.gk;
       }
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.s_full[tile]), (uint32_t)i & 1u, abort_flag, kWaitNs))) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.s_full[tile][i & 1]), (uint32_t)(i >> 1) & 1u, abort_flag,
+                                             kWaitNs))) {
         ok = false;
         break;
       }
       fence_after();
-      float s[128];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ld_x32(ts + 32 * k, s + 32 * k);
+      const uint32_t si = ts + (i & 1) * kTileKeys;
+      float s[kTileKeys];
+      ld_x32(si, s);
+      ld_x32(si + 32, s + 32);
       ld_wait();
+      ld_tie(s);
+      ld_tie(s + 32);
+      float top, scale = mul, shift = bias;
+      if (st.full && !kExtras) {
+        float t0 = s[0], t1 = s[1];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ld_tie(s + 32 * k);
-      float top = -INFINITY, scale = mul, shift = bias;
-      const bool capped = kExtras && p.cap > 0.0f, biased = kExtras && p.slopes;
-      if (st.full && !capped && !biased) {
-        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
-#pragma unroll
-        for (int k = 4; k < 128; k += 8) {
-          t0 = fmaxf(t0, fmaxf(s[k], s[k + 1]));
-          t1 = fmaxf(t1, fmaxf(s[k + 2], s[k + 3]));
-          if (k + 4 < 128) {
-            t2 = fmaxf(t2, fmaxf(s[k + 4], s[k + 5]));
-            t3 = fmaxf(t3, fmaxf(s[k + 6], s[k + 7]));
-          }
+        for (int e = 2; e + 3 < kTileKeys; e += 4) {
+          t0 = fmaxf(t0, fmaxf(s[e], s[e + 1]));
+          t1 = fmaxf(t1, fmaxf(s[e + 2], s[e + 3]));
         }
-        top = fmaf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), mul, bias);
+        top = fmaf(fmaxf(fmaxf(t0, t1), fmaxf(s[kTileKeys - 2], s[kTileKeys - 1])), mul, bias);
       } else {
-        // visible: keys [lo, hi) of the step, and those below pre
-        int lo = 0, hi = st.n, pre = 0;
+        // cap, bias and mask: raw products to log2 units, with -inf where the row does not see the key
         const int kp0 = p.pos[st.seg] + st.t0;
+#pragma unroll
+        for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(s[e], mul, bias);
+        if (kExtras && p.cap > 0.0f) {
+          const float twice = 2.0f * kLog2e / p.cap, cap = p.cap * kLog2e;
+#pragma unroll
+          for (int e = 0; e < kTileKeys; ++e) s[e] = softcap(s[e], cap, twice);
+        }
+        if (kExtras && p.slopes) {
+          const float d0 = (float)(qpos - kp0);
+#pragma unroll
+          for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(-slope, fabsf(d0 - (float)e), s[e]);
+        }
         if (!st.full) {
+          // visible: keys [lo, hi) of the step, and those below pre
+          int lo = 0, hi = st.n, pre = 0;
           if (p.causal) hi = (int)min((int64_t)hi, (int64_t)qpos - kp0 + 1);
           if (p.window) lo = (int)max((int64_t)0, (int64_t)qpos - kp0 - p.window + 1);
           if (p.prefix > kp0) pre = min(p.prefix - kp0, st.n);
-        }
 #pragma unroll
-        for (int k = 0; k < 128; ++k) {
-          float x = fmaf(s[k], mul, bias);
-          if (capped) x = softcap(x, p.cap, rcap) * kLog2e;
-          if (biased) x = fmaf(-slope, fabsf((float)(qpos - kp0 - k)), x);
-          if (!st.full) {
-            bool see = k < pre || (k >= lo && k < hi);
-            if (kExtras && p.k_doc) see = see && __ldg(p.k_doc + key_base + st.t0 + min(k, st.n - 1)) == qdoc;
-            x = see ? x : -INFINITY;
+          for (int w = 0; w < 2; ++w) {
+            auto below = [&](int c) { c -= 32 * w; return c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u; };
+            uint32_t see = (below(hi) & ~below(lo)) | below(pre);
+            if (kExtras && p.k_doc) {
+              const int doc = p.k_doc[key_base + st.t0 + min(32 * w + lane, st.n - 1)];
+              const int row0 = __shfl_sync(0xFFFFFFFFu, qdoc, 0);
+              if (__all_sync(0xFFFFFFFFu, qdoc == row0)) {  // the warp's rows are of one document
+                see &= __ballot_sync(0xFFFFFFFFu, doc == row0);
+              } else {
+                uint32_t same = 0;
+#pragma unroll 4
+                for (int e = 0; e < 32; ++e) same |= (uint32_t)(__shfl_sync(0xFFFFFFFFu, doc, e) == qdoc) << e;
+                see &= same;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * w + e] = (see >> e) & 1u ? s[32 * w + e] : -INFINITY;
           }
-          s[k] = x;
-          top = fmaxf(top, x);
         }
+        top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kTileKeys; e += 2) top = fmaxf(top, fmaxf(s[e], s[e + 1]));
         scale = 1.0f;
         shift = 0.0f;
       }
@@ -548,17 +573,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         const float alpha = grow ? ex2(m - need) : 1.0f;
         if (grow) m = need;
         l *= alpha;
-        if (i > 0) {
+        if (i > 0) {  // the output of the step before has to be complete
+          if (!__all_sync(0xFFFFFFFFu,
+                          mbar_wait(smem_u32(&ct.o_done[tile]), (uint32_t)(i - 1) & 1u, abort_flag, kWaitNs))) {
+            ok = false;
+            break;
+          }
+          fence_after();
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            float o[32];
-            ld_x32(to + 32 * k, o);
+          for (int k = 0; k < kD; k += 16) {
+            float o[16];
+            ld_x16(to + k, o);
             ld_wait();
-            ld_tie(o);
-            uint32_t w[32];
+            ld_tie16(o);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
-            st_x32(to + 32 * k, w);
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+            st_x16(to + k, w);
           }
         }
       }
@@ -566,32 +597,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       const float c0 = shift - ref;
       float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
+      for (int k = 0; k < 2; ++k) {
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          float* x = s + 64 * half + k;
+        for (int e = 0; e < 32; e += 4) {
+          float* x = s + 32 * k + e;
           fma2(x[0], x[1], x[0], x[1], scale, scale, c0, c0);
           fma2(x[2], x[3], x[2], x[3], scale, scale, c0, c0);
           x[0] = ex2(x[0]), x[1] = ex2(x[1]), x[2] = ex2(x[2]), x[3] = ex2(x[3]);
           add2(sum0, sum1, sum0, sum1, x[0], x[1]);
           add2(sum2, sum3, sum2, sum3, x[2], x[3]);
-          w[k / 2] = pack_f16x2(x[0], x[1]);
-          w[k / 2 + 1] = pack_f16x2(x[2], x[3]);
+          w[e / 2] = pack_f16x2(x[0], x[1]);
+          w[e / 2 + 1] = pack_f16x2(x[2], x[3]);
         }
         if (vzero) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = 0;
+          for (int e = 0; e < 16; ++e) w[e] = 0;
         }
-        st_x32(ts + 32 * half, w);
+        st_x16(si + 16 * k, w);
       }
       l = fmaf((sum0 + sum1) + (sum2 + sum3), inv, l);
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ct.p_ready[tile]));
+      if (lane == 0) mbar_arrive(smem_u32(&ct.p_ready[tile][i & 1]));
     }
-    if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.done), 0, abort_flag, kWaitNs))) ok = false;
+    // a tile's own work; where the two are joined through the key buffers, the other's too
+    for (int t = 0; t < 2 && ok; ++t) {
+      if (kPair && (t != tile || (t == 1 && !two))) continue;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.done[t]), 0, abort_flag, kWaitNs));
+    }
     if (!ok) {
       if (lane == 0) set_status(p.status, kStatusTimeout);
       *abort_flag = 1;

@@ -33,6 +33,13 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   return v;
 }
 
+// Read-only 2-byte load that stays where it is written: issued ahead of its use on purpose.
+__device__ __forceinline__ uint32_t ldg_nc_u16(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
 // Read-only 16-byte load that may allocate in L1: for access patterns where one
 // warp instruction uses half of each 32-byte sector and the next uses the rest.
 __device__ __forceinline__ uint4 ldg_nc_v4_l1(const void* p) {

@@ -1,12 +1,16 @@
 // attend.cu — softmax attention of few query rows over a window of the NVFP4 cache, the
 // drafted tokens of a tree, and the joining of partial results (attend.cuh gives the formulas).
 #include <algorithm>
+#include <atomic>
 
 #include "attend.cuh"
+#include "tc.cuh"
 
 namespace nvfp4 {
 namespace attend {
 namespace {
+
+using tc::smem_u32;
 
 constexpr int kRows = 16;       // query rows of a CTA: the M of one mma.sync
 constexpr int kStep = 32;       // keys a warp takes at a time
@@ -36,31 +40,62 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
 
+// A warp's ring of key steps on their way from the cache: codes, scales and what the step is.
+constexpr int kRing = 4;
+struct Stage {
+  uint8_t k_codes[kStep * 64], v_codes[kStep * 64];
+  uint8_t k_scales[kStep * 8], v_scales[kStep * 8];
+};
+struct StepInfo {
+  int32_t seg, t0, n, vis;  // n == 0: no more steps
+};
+
 struct Shared {
-  SlotView view[kMaxWindowSlots];
-  float m[kWarps][kRows], l[kWarps][kRows];
-  int32_t row_pos[kRows], row_doc[kRows];
   union {
+    Stage ring[kWarps][kRing];
     float o[kWarps][kRows][kD];
     struct {
       int32_t parents[kMaxTreeDrafts];
       int16_t list[kWarps][kMaxTreeDrafts];
     } tree;
   };
+  StepInfo info[kWarps][kRing];
+  SlotView view[kMaxWindowSlots];
+  float m[kWarps][kRows], l[kWarps][kRows];
+  int32_t row_pos[kRows], row_doc[kRows];
 };
+
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Within an 8-key tile the product's column 2 c + e is key c + 4 e: the lanes of one read of V then
+// take neighbouring keys.
+__device__ __forceinline__ int tile_key(int n) { return (n >> 1) + 4 * (n & 1); }
 
 // One CTA: 16 query rows of one cache head against a range of the window's 32-key steps, the
 // steps dealt out to four warps.  mma.sync and not tcgen05: with at most 16 rows the kernel
 // waits for the cache's bytes and for their decoding, and mma.sync takes the decoded codes from
 // registers, where tcgen05 would have them stored to shared memory first.
+// Each warp copies its steps' codes and scales into its own ring three steps ahead (cp.async: no
+// registers, and no barrier but the warp's own).
 // Lane (g, c) = (lane / 4, lane % 4).  Scores: the contraction runs over dims in an order in
 // which lane c owns dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of key g of an
 // 8-key tile.  Values: lane (g, c) owns dims 16 g .. 16 g + 15 (8 bytes, one scale) of keys
-// 2 c, 2 c + 1 of a tile; nibbles of the two keys are interleaved before the conversion, which
-// then yields the (key, key + 1) pairs the product wants.
+// c, c + 4 of a tile; nibbles of the two keys are interleaved before the conversion, which
+// then yields the pairs of columns the product wants.
 template <bool kExtras>  // a cap, a bias or documents
 __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_constant__ Params p) {
-  __shared__ Shared sh;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,20 +177,60 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
   const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
-  int seg = 0, seg_at = -1;
+  const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
+  // next step that some row sees, into ring place `to`
+  int next = first + warp, next_seg = 0;
+  auto issue = [&](int to) {
+    StepInfo si = {0, 0, 0, 0};
+    for (; next < last; next += kWarps) {
+      while (next >= p.step_end[next_seg]) ++next_seg;
+      if (!sh.view[next_seg].ok) continue;
+      const int t0 = (next - (next_seg ? p.step_end[next_seg - 1] : 0)) * kStep;
+      const int n = min(kStep, p.tokens[next_seg] - t0);
+      const int kp0 = p.pos[next_seg] + t0;
+      const int vis = visibility(p, kp0, kp0 + n - 1, q_first, q_last);
+      if (vis == 0) continue;
+      si = {next_seg, t0, n, n < kStep || (kExtras && p.k_doc) ? 1 : vis};
+      next += kWarps;
+      break;
+    }
+    if (si.n > 0) {
+      Stage& st = sh.ring[warp][to];
+      const int64_t slot = p.slots[si.seg], row0 = (int64_t)si.t0 * p.heads + h;
+      const uint8_t* kc = p.base + p.off_k_codes + slot * p.slot_codes + row0 * (kD / 2) + 16 * c;
+      const uint8_t* vc = p.base + p.off_v_codes + slot * p.slot_codes + row0 * (kD / 2) + 16 * c;
+      const uint8_t* ks = p.base + p.off_k_scales + slot * p.slot_scales + row0 * (kD / 16);
+      const uint8_t* vs = p.base + p.off_v_scales + slot * p.slot_scales + row0 * (kD / 16);
+      const uint32_t kd = smem_u32(st.k_codes), vd = smem_u32(st.v_codes);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {  // keys behind the step's last repeat it and are masked
+        copy_16(kd + (32 * t + lane) * 16, kc + min(8 * t + tile_key(g), si.n - 1) * code_step);
+        const int key = 8 * t + g;
+        copy_16(vd + key * 64 + ((c ^ (key & 2)) << 4), vc + min(key, si.n - 1) * code_step);
+      }
+      copy_8(smem_u32(st.k_scales) + lane * 8, ks + min((lane & ~7) + tile_key(lane & 7), si.n - 1) * scale_step);
+      copy_8(smem_u32(st.v_scales) + lane * 8, vs + min(lane, si.n - 1) * scale_step);
+    }
+    if (lane == 0) sh.info[warp][to] = si;
+    copy_commit();
+  };
+  int seg_at = -1, key_seg = 0;
   float bias[2] = {0.0f, 0.0f}, mul[2] = {0.0f, 0.0f}, lg = 0.0f, inv = 1.0f;
-  int64_t key_base = 0;  // keys listed before the slot
+  int64_t key_base = 0;  // keys listed before slot key_seg
   bool vzero = false;
   const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-  for (int st = first + warp; st < last; st += kWarps) {
-    while (st >= p.step_end[seg]) key_base += p.tokens[seg++];
-    const int t0 = (st - (seg ? p.step_end[seg - 1] : 0)) * kStep;  // first token of the step in its slot
-    const int n = min(kStep, p.tokens[seg] - t0);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
+  for (int at = 0;; at = (at + 1) % kRing) {
+    copy_wait<kRing - 2>();
+    __syncwarp();
+    const StepInfo si = sh.info[warp][at];
+    if (si.n == 0) break;
+    const int seg = si.seg, t0 = si.t0, n = si.n, vis = si.vis;
     const int kp0 = p.pos[seg] + t0;
-    if (!sh.view[seg].ok) continue;
-    int vis = visibility(p, kp0, kp0 + n - 1, q_first, q_last);
-    if (vis == 0) continue;
-    if (n < kStep || (kExtras && p.k_doc)) vis = 1;
+    if (kExtras && p.k_doc)
+      for (; key_seg < seg; ++key_seg) key_base += p.tokens[key_seg];
+    const Stage& stage = sh.ring[warp][at];
     if (seg != seg_at) {  // the slot's scales and q . mu of this lane's rows
       seg_at = seg;
       const SlotView sv = sh.view[seg];
@@ -182,37 +257,16 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
         mul[u] = f * sv.gk;
       }
     }
-    const int64_t row0 = ((int64_t)t0 * p.heads + h);
-    const uint8_t* kc = p.base + p.off_k_codes + p.slots[seg] * p.slot_codes + row0 * (kD / 2);
-    const uint8_t* vc = p.base + p.off_v_codes + p.slots[seg] * p.slot_codes + row0 * (kD / 2);
-    const uint8_t* ks_ = p.base + p.off_k_scales + p.slots[seg] * p.slot_scales + row0 * (kD / 16);
-    const uint8_t* vs_ = p.base + p.off_v_scales + p.slots[seg] * p.slot_scales + row0 * (kD / 16);
-    const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
-
-    // scores of 4 tiles of 8 keys (rows behind the slot's last token repeat it and are masked)
+    // scores of 4 tiles of 8 keys
     float s[4][4];
-    uint4 kw[4];
-    uint32_t kb[4];
-    uint2 vw[8];
-    uint32_t vb[8];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int key = min(8 * t + g, n - 1);
-      kw[t] = ldg_nc_v4(kc + key * code_step + 16 * c);
-      kb[t] = *reinterpret_cast<const uint16_t*>(ks_ + key * scale_step + 2 * c);
-    }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int key = min(8 * (t >> 1) + 2 * c + (t & 1), n - 1);
-      vw[t] = __ldg(reinterpret_cast<const uint2*>(vc + key * code_step + 8 * g));
-      vb[t] = vs_[key * scale_step + g];
-    }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[t][k] = 0.0f;
-      const uint32_t words[4] = {kw[t].x, kw[t].y, kw[t].z, kw[t].w};
-      const uint32_t s2[2] = {e4m3_to_f16x2_bcast(kb[t] & 0xFFu), e4m3_to_f16x2_bcast(kb[t] >> 8)};
+      const uint4 kw = *reinterpret_cast<const uint4*>(stage.k_codes + (32 * t + lane) * 16);
+      const uint32_t kb = *reinterpret_cast<const uint16_t*>(stage.k_scales + (8 * t + g) * 8 + 2 * c);
+      const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
+      const uint32_t s2[2] = {e4m3_to_f16x2_bcast(kb & 0xFFu), e4m3_to_f16x2_bcast(kb >> 8)};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t b[4];
@@ -221,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
         mma_f16(s[t], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2], qa[2 * w + 1][3], b[2], b[3]);
       }
     }
-    // element k of a tile: row g + 8 (k / 2), key 2 c + k % 2
+    // element k of a tile: row g + 8 (k / 2), key c + 4 (k % 2)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int u = k >> 1, key = 8 * t + 2 * c + (k & 1);
+        const int u = k >> 1, key = 8 * t + c + 4 * (k & 1);
         float x = fmaf(s[t][k], mul[u], bias[u]);
         if (kExtras) {
           if (p.cap > 0.0f) x = softcap(x, p.cap, rcap) * kLog2e;
@@ -271,40 +325,47 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
         o[j][3] *= alpha[1];
       }
     }
-    if (vzero) continue;
+    if (!vzero) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {  // 16 keys: tiles 2 ks and 2 ks + 1
       const uint32_t a0 = pack_f16x2(s[2 * ks][0], s[2 * ks][1]), a1 = pack_f16x2(s[2 * ks][2], s[2 * ks][3]);
       const uint32_t a2 = pack_f16x2(s[2 * ks + 1][0], s[2 * ks + 1][1]);
       const uint32_t a3 = pack_f16x2(s[2 * ks + 1][2], s[2 * ks + 1][3]);
-      uint32_t b[2][16];  // [tile][dim of the lane's block]
+      uint2 wa[2], wb[2];
+      uint32_t s2[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint2 wa = vw[4 * ks + 2 * t], wb = vw[4 * ks + 2 * t + 1];
-        uint32_t s2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-            : "=r"(s2)
-            : "h"((uint16_t)(vb[4 * ks + 2 * t] | (vb[4 * ks + 2 * t + 1] << 8))));
-        const uint32_t xa[2] = {wa.x, wa.y}, xb[2] = {wb.x, wb.y};
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t even[4], odd[4];
-          e2m1x8_times_scale((xa[w] & 0x0F0F0F0Fu) | ((xb[w] << 4) & 0xF0F0F0F0u), s2, even);
-          e2m1x8_times_scale(((xa[w] >> 4) & 0x0F0F0F0Fu) | (xb[w] & 0xF0F0F0F0u), s2, odd);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            b[t][8 * w + 2 * k] = even[k];
-            b[t][8 * w + 2 * k + 1] = odd[k];
-          }
-        }
+        const int key = 16 * ks + 8 * t + c;  // and key + 4
+        const int off = (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1);
+        wa[t] = *reinterpret_cast<const uint2*>(stage.v_codes + key * 64 + off);
+        wb[t] = *reinterpret_cast<const uint2*>(stage.v_codes + (key + 4) * 64 + off);
+        const uint32_t pair = stage.v_scales[key * 8 + g] | ((uint32_t)stage.v_scales[(key + 4) * 8 + g] << 8);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[t]) : "h"((uint16_t)pair));
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mma_f16(o[j], a0, a1, a2, a3, b[0][j], b[1][j]);
+      for (int w = 0; w < 2; ++w) {  // 8 dims of the lane's block at a time
+        uint32_t even[2][4], odd[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t xa = w ? wa[t].y : wa[t].x, xb = w ? wb[t].y : wb[t].x;
+          e2m1x8_times_scale((xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u), s2[t], even[t]);
+          e2m1x8_times_scale(((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u), s2[t], odd[t]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_f16(o[8 * w + 2 * k], a0, a1, a2, a3, even[0][k], even[1][k]);
+          mma_f16(o[8 * w + 2 * k + 1], a0, a1, a2, a3, odd[0][k], odd[1][k]);
+        }
+      }
     }
+    }
+    __syncwarp();
+    issue((at + kRing - 1) % kRing);
   }
+  copy_wait<0>();
 
   // join the warps: element k of o[j]: row g + 8 (k / 2), dim 32 c + 16 (k % 2) + j
-  __syncthreads();  // the drafts' parents share this memory
+  __syncthreads();  // the rings share this memory
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float ls = quad_sum(l[u]);
@@ -342,18 +403,25 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   }
 }
 
-// Joins the partial results: one warp a row, O = sum_i 2^(L_i - L) O_i, L = log2 sum_i 2^L_i,
-// in the order of the parts.
+// Joins the partial results: O = sum_i 2^(L_i - L) O_i, L = log2 sum_i 2^L_i.  kSplit warps of a CTA
+// of eight share a row's parts (each taking every kSplit-th, eight reads in flight) and add their
+// sums in a fixed order.
+template <int kSplit>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kJoin = 8;
+  __shared__ float4 part[kSplit > 1 ? 8 : 1][32];
+  __shared__ float part_sum[8];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = (int64_t)p.heads * p.rows;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= n) return;
+  const int64_t row = (int64_t)blockIdx.x * (8 / kSplit) + warp / kSplit;
+  const int w = warp % kSplit;
+  const bool live = row < n;
+  const int64_t rr = live ? row : n - 1;
   float top = -INFINITY;
   for (int i = lane; i < p.parts; i += 32) {
-    const float l = p.part_l[i * n + row];
+    const float l = p.part_l[i * n + rr];
     top = l != l || top != top ? NAN : fmaxf(top, l);
   }
 #pragma unroll
@@ -361,28 +429,48 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const float v = __shfl_xor_sync(0xFFFFFFFFu, top, x);
     top = v != v || top != top ? NAN : fmaxf(top, v);
   }
+  const float ref = top == -INFINITY ? 0.0f : top;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float sum = 0.0f;
-  if (top != -INFINITY) {
-    for (int i = 0; i < p.parts; ++i) {
-      const float l = p.part_l[i * n + row];
-      if (l == -INFINITY) continue;
-      const float f = ex2(l - top);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (i * n + row) * kD + 4 * lane);
-      sum += f;
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+  for (int i0 = w; i0 < p.parts; i0 += kSplit * kJoin) {
+    float f[kJoin];
+    float4 v[kJoin];
+#pragma unroll
+    for (int e = 0; e < kJoin; ++e) {
+      const int i = i0 + e * kSplit < p.parts ? i0 + e * kSplit : i0;
+      f[e] = p.part_l[i * n + rr];
+      v[e] = *reinterpret_cast<const float4*>(p.part_o + (i * n + rr) * kD + 4 * lane);
     }
-    const float f = 1.0f / sum;
-    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+    for (int e = 0; e < kJoin; ++e) {
+      if (i0 + e * kSplit >= p.parts) break;
+      f[e] = ex2(f[e] - ref);  // 0 for a part that saw nothing, whose O is 0 as well
+      sum += f[e];
+      acc.x = fmaf(f[e], v[e].x, acc.x);
+      acc.y = fmaf(f[e], v[e].y, acc.y);
+      acc.z = fmaf(f[e], v[e].z, acc.z);
+      acc.w = fmaf(f[e], v[e].w, acc.w);
+    }
   }
+  if (kSplit > 1) {
+    part[warp][lane] = acc;
+    if (lane == 0) part_sum[warp] = sum;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int e = 1; e < kSplit; ++e) {
+      const float4 v = part[warp + e][lane];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      sum += part_sum[warp + e];
+    }
+  }
+  if (!live) return;
+  const float f = top == -INFINITY ? 0.0f : 1.0f / sum;
   const int h = (int)(row / p.rows);
   const int64_t r = row - (int64_t)h * p.rows, i = r / p.group;
   const int head = h * p.group + (int)(r - i * p.group);
   stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + 4 * lane) * 2,
-         make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w)));
+         make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f)));
   if (lane == 0 && p.lse) p.lse[(int64_t)head * p.tq + i] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
@@ -427,6 +515,21 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   }
   plan.splits = (int32_t)std::max<int64_t>(splits, 1);
   return plan;
+}
+
+template <bool kExtras>
+cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_relaxed)) {  // doing it twice is harmless
+    e = cudaFuncSetAttribute(attend_rows_kernel<kExtras>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  return launch_pdl(attend_rows_kernel<kExtras>, grid, kThreads, sizeof(Shared), s, p);
 }
 
 }  // namespace
@@ -497,11 +600,13 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   const dim3 grid(p.parts, p.heads);
   cudaError_t e;
   if (plan.tiles) e = launch_attend_tiles(p, s);
-  else if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_pdl(attend_rows_kernel<true>, grid, kThreads, 0, s, p);
-  else e = launch_pdl(attend_rows_kernel<false>, grid, kThreads, 0, s, p);
+  else if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_rows<true>(p, grid, s);
+  else e = launch_rows<false>(p, grid, s);
   if (e != cudaSuccess || p.parts == 1) return e;
   const int64_t n = (int64_t)p.heads * p.rows;
-  return launch_pdl(attend_join_kernel, dim3((unsigned)((n + 7) / 8)), 256, 0, s, p);
+  // few parts: a warp a row; more: eight warps share a row's
+  if (p.parts <= 8) return launch_pdl(attend_join_kernel<1>, dim3((unsigned)((n + 7) / 8)), 256, 0, s, p);
+  return launch_pdl(attend_join_kernel<8>, dim3((unsigned)n), 256, 0, s, p);
 }
 
 }  // namespace nvfp4

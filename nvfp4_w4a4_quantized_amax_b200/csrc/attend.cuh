@@ -30,6 +30,7 @@ struct Params {
   const uint8_t* base;
   int64_t off_k_codes, off_v_codes, off_k_scales, off_v_scales, off_mu, off_gscale, off_tokens;
   int64_t slot_codes, slot_scales;
+  int64_t chunk;  // tokens of a slot
   int32_t heads, group;  // cache heads, query heads of each
   int32_t n_slots;
   int32_t slots[kMaxWindowSlots];
@@ -242,7 +243,7 @@ __device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parent
 // Tensor-core form for many rows (attend_tiles.cu): key steps of kTileKeys, at most kMaxListed of
 // them a CTA.
 constexpr int kTileKeys = 64;
-constexpr int kMaxListed = 4096;
+constexpr int kMaxListed = 2048;
 constexpr int64_t kTileRows = 128;
 cudaError_t launch_attend_tiles(const Params& p, cudaStream_t s);
 

@@ -1,5 +1,7 @@
 // attend_tiles.cu — softmax attention of many query rows over a window of the NVFP4 cache, on the
 // fifth-generation tensor cores (attend.cuh gives the formulas).
+#include <stddef.h>
+
 #include <atomic>
 
 #include "attend.cuh"
@@ -11,10 +13,11 @@ namespace {
 
 using namespace tc;
 
-// One CTA of four warpgroups, one CTA an SM, in steps of 64 keys:
+// One CTA of five warpgroups, one CTA an SM, in steps of 64 keys:
 //   warps 0..3, 4..7  softmax of two tiles of 128 rows: thread = row
-//   warps 8..11       decode the window's K and V to binary16 e2m1 * s in shared memory
-//   warps 12, 13      issue the tensor core's work of a tile each: S = Q K~^T and O += P V~
+//   warps 8..11       decode the window's K to binary16 e2m1 * s in shared memory, 12..15 its V
+//                     (one group doing both in turn was the slowest part of a step)
+//   warps 16, 17      issue the tensor core's work of a tile each: S = Q K~^T and O += P V~
 // Tensor memory holds, for each tile, two score buffers of 64 columns and the output (128).  The
 // weights P (binary16) take the place of the scores they come from and are the A operand of the
 // second product straight from there.  With two buffers the scores of the next step are ready
@@ -25,7 +28,8 @@ using namespace tc;
 //           the end.
 // Both operands of both products are in the 128-byte swizzle: K~ as rows of keys (K-major), V~
 // the same way, which for O += P V~ is the MN-major B operand, so one decoder writes both.
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kIssueWarp = 16;
 constexpr int kQBytes = 128 * kD * 2;        // 32 KB: two 128-row x 128-byte blocks
 constexpr int kQBlock = 128 * 128;
 constexpr int kKvBytes = kTileKeys * kD * 2;  // 16 KB: two 64-row x 128-byte blocks
@@ -34,9 +38,10 @@ constexpr int kStages = 4;
 constexpr int kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// Registers: the launch's 128 a thread are moved between the warpgroups.
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 168, kRegsDecode = 104, kRegsIssue = 72;
-static_assert(2 * kRegsSoftmax + kRegsDecode + kRegsIssue == 4 * kRegsLaunch, "the register split must balance");
+// Registers: the launch's 96 a thread (20 warps, five on each of the SM's four files) are moved
+// between the warpgroups.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsDecode = 72, kRegsIssue = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsIssue == 5 * kRegsLaunch, "the register split must balance");
 
 // The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
 // rarely rescaled; a row's largest weight is then between 2^kUp and 2^(kUp + kLazy) = 2^14.
@@ -55,7 +60,7 @@ struct Control {
 constexpr int kControlBytes = (sizeof(Control) + 127) / 128 * 128;
 
 constexpr int smem_bytes(bool pair) {
-  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 4;
+  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 8;
 }
 
 // Instruction descriptor: D FP32 (bits 4..5 = 1), A and B binary16 (0), N >> 3, M >> 4; bit 16: B
@@ -132,25 +137,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// A listed key step: its number in the CTA's range (bits 0..11), list entry of its slot (12..18),
-// and whether every row sees all of it (20).
-__device__ __forceinline__ uint32_t listed_step(int rel, int seg, bool full) {
-  return (uint32_t)rel | ((uint32_t)seg << 12) | (full ? 1u << 20 : 0u);
-}
-
-struct Step {
-  int seg, t0, n;  // slot entry, first token in the slot, tokens
-  bool full;
-};
-__device__ __forceinline__ Step read_step(const Params& p, const uint32_t* list, int i, int first) {
-  const uint32_t v = list[i];
-  Step s;
-  s.seg = (int)((v >> 12) & 0x7Fu);
-  const int st = first + (int)(v & 0xFFFu);
-  s.t0 = (st - (s.seg ? p.step_end[s.seg - 1] : 0)) * kTileKeys;
-  s.n = min(kTileKeys, p.tokens[s.seg] - s.t0);
-  s.full = (v >> 20) & 1u;
-  return s;
+// A listed key step: the cache row (slot * chunk_tokens + token) of its first key; its number of
+// keys (bits 0..7), list entry of its slot (8..15) and whether every row sees all of it (16).
+__device__ __forceinline__ uint2 listed_step(uint32_t row, int n, int seg, bool full) {
+  return make_uint2(row, (uint32_t)n | ((uint32_t)seg << 8) | (full ? 1u << 16 : 0u));
 }
 
 template <bool kExtras, bool kPair>
@@ -162,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   uint8_t* kbuf = qbuf + (kPair ? 2 : 1) * kQBytes;
   uint8_t* vbuf = kbuf + kStages * kKvBytes;
   Control& ct = *reinterpret_cast<Control*>(vbuf + kStages * kKvBytes);
-  uint32_t* list = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&ct) + kControlBytes);
+  uint2* list = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(&ct) + kControlBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x, h = blockIdx.y;
   const int64_t r0 = (int64_t)blockIdx.z * (kPair ? 256 : 128);
@@ -187,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   const bool two = kPair && r_end - r0 > 128;  // the second tile of a pair has rows
   if (threadIdx.x == 0) {
     for (int b = 0; b < kStages; ++b) {
-      mbar_init(smem_u32(&ct.k_full[b]), 4);
+      mbar_init(smem_u32(&ct.k_full[b]), 2);
       mbar_init(smem_u32(&ct.k_empty[b]), two ? 2 : 1);  // tiles that take a step
-      mbar_init(smem_u32(&ct.v_full[b]), 4);
+      mbar_init(smem_u32(&ct.v_full[b]), 2);
       mbar_init(smem_u32(&ct.v_empty[b]), two ? 2 : 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -205,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     ct.q_last = ct.d_last = -0x7FFFFFFF - 1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ct.tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -317,7 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       const int rel = b + lane;
       const int vis = rel < n_range ? flags[rel] : 0;
       const unsigned seen = __ballot_sync(0xFFFFFFFFu, vis != 0);
-      if (vis) list[n + __popc(seen & ((1u << lane) - 1u))] = listed_step(rel, segs[rel], vis == 2);
+      if (vis) {
+        const int seg = segs[rel];
+        const int t0 = (first + rel - (seg ? p.step_end[seg - 1] : 0)) * kTileKeys;
+        list[n + __popc(seen & ((1u << lane) - 1u))] =
+            listed_step((uint32_t)((int64_t)p.slots[seg] * p.chunk + t0), min(kTileKeys, p.tokens[seg] - t0), seg, vis == 2);
+      }
       n += __popc(seen);
     }
     if (lane == 0) ct.listed = n;
@@ -329,49 +324,66 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   const int n = ct.listed;
   volatile int* abort_flag = &ct.abort;
 
-  if (warp >= 12) {
+  if (warp >= kIssueWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    const int t = warp - 12;
+    const int t = warp - kIssueWarp;
     if (t < (two || !kPair ? 2 : 1) && lane == 0) {
       // ---------------------------------------------------- tensor core, tile t
-      bool ok = true;
-      auto wait = [&](uint64_t& bar, int phase) {
-        if (ok && !mbar_wait(smem_u32(&bar), (uint32_t)phase & 1u, abort_flag, kWaitNs)) ok = false;
-        return ok;
-      };
+      // Few instructions between a wait and what it lets go: the other warps leave this one few issue
+      // slots.  The loop is unrolled over the ring, so buffers and barriers are constants.
       const uint32_t hi = (uint32_t)(smem_desc(0, 0, 1024, 2) >> 32);
       const uint32_t q_lo = (uint32_t)smem_desc(smem_u32(qbuf + (kPair ? t : 0) * kQBytes), 16, 1024, 2);
-      const uint32_t k_lo = (uint32_t)smem_desc(smem_u32(kbuf), 16, 1024, 2);
-      const uint32_t v_lo = (uint32_t)smem_desc(smem_u32(vbuf), kKvBlock, 1024, 2);
+      // a pair's tiles both take every step; else tile t takes steps t, t + 2, ...: buffers t, t + 2
+      const uint32_t k_lo = (uint32_t)smem_desc(smem_u32(kbuf) + (kPair ? 0 : t * kKvBytes), 16, 1024, 2);
+      const uint32_t v_lo = (uint32_t)smem_desc(smem_u32(vbuf) + (kPair ? 0 : t * kKvBytes), kKvBlock, 1024, 2);
       const uint32_t ts = tmem + t * 128, to = tmem + 256 + t * 128;
-      // a pair's tiles both take every step; else tile t takes steps t, t + 2, ...
+      const uint32_t bars = smem_u32(&ct) + (kPair ? 0 : 8 * t), tbars = smem_u32(&ct) + 16 * t;
+      constexpr uint32_t kKFull = offsetof(Control, k_full), kKEmpty = offsetof(Control, k_empty);
+      constexpr uint32_t kVFull = offsetof(Control, v_full), kVEmpty = offsetof(Control, v_empty);
+      constexpr uint32_t kSFull = offsetof(Control, s_full), kPReady = offsetof(Control, p_ready);
+      constexpr int kMine = kPair ? kStages : kStages / 2, kStride = kPair ? 1 : 2;  // ring buffers of a tile
+      const uint32_t o_done = smem_u32(&ct.o_done[t]);
       const int n_mine = kPair ? n : (n + 1 - t) / 2;
-      auto scores = [&](int i) {  // S_t = Q_t K~^T of this tile's step i, 16 dims an instruction
-        const int step = kPair ? i : 2 * i + t, b = step % kStages;
-        if (!wait(ct.k_full[b], step / kStages)) return;
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, abort_flag, kWaitNs)) ok = false;
+      };
+      auto scores = [&](int e, uint32_t parity) {  // S_t = Q_t K~^T from this tile's ring buffer e
+        wait(bars + kKFull + 8 * kStride * e, parity);
         fence_after();
-        const uint32_t k = k_lo + b * (kKvBytes >> 4), d = ts + (i & 1) * kTileKeys;
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk)
-          mma_ss(d, descriptor(q_lo + (((kk >> 2) * kQBlock + (kk & 3) * 32) >> 4), hi),
-                 descriptor(k + (((kk >> 2) * kKvBlock + (kk & 3) * 32) >> 4), hi), kk > 0);
-        commit(smem_u32(&ct.s_full[t][i & 1]));
-        commit(smem_u32(&ct.k_empty[b]));
+          mma_ss(ts + (e & 1) * kTileKeys, descriptor(q_lo + (((kk >> 2) * kQBlock + (kk & 3) * 32) >> 4), hi),
+                 descriptor(k_lo + ((kStride * e * kKvBytes + (kk >> 2) * kKvBlock + (kk & 3) * 32) >> 4), hi), kk > 0);
+        commit(tbars + kSFull + 8 * (e & 1));
+        commit(bars + kKEmpty + 8 * kStride * e);
       };
-      for (int i = 0; i < 2 && i < n_mine; ++i) scores(i);
-      for (int i = 0; i < n_mine && ok; ++i) {  // O_t += P_t V~, 16 keys an instruction
-        const int step = kPair ? i : 2 * i + t, b = step % kStages;
-        if (!wait(ct.v_full[b], step / kStages) || !wait(ct.p_ready[t][i & 1], i >> 1)) break;
-        fence_after();
-        const uint32_t v = v_lo + b * (kKvBytes >> 4), a = ts + (i & 1) * kTileKeys;
+      if (n_mine > 0) scores(0, 0);
+      if (n_mine > 1) scores(1 % kMine, (uint32_t)(1 / kMine) & 1u);
+      uint32_t ring = 0;  // parity of the ring's round
+      for (int i0 = 0; i0 < n_mine && ok; i0 += kMine, ring ^= 1u) {
 #pragma unroll
-        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          mma_ts(to, a + kk * 8, descriptor(v + kk * (2048 >> 4), hi), i > 0 || kk > 0);
-        commit(smem_u32(&ct.o_done[t]));
-        commit(smem_u32(&ct.v_empty[b]));
-        // the next scores take the buffer whose weights this reads; the two products differ in shape,
-        // so only completion orders them (the scores of step i + 1 are there already)
-        if (i + 2 < n_mine && wait(ct.o_done[t], i)) scores(i + 2);
+        for (int e = 0; e < kMine; ++e) {
+          const int i = i0 + e;
+          if (i >= n_mine || !ok) break;
+          // O_t += P_t V~, 16 keys an instruction
+          const uint32_t half = kMine == 4 ? (uint32_t)(e >> 1) : ring;  // parity of score buffer e & 1
+          wait(bars + kVFull + 8 * kStride * e, ring);
+          wait(tbars + kPReady + 8 * (e & 1), half);
+          fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTileKeys / 16; ++kk)
+            mma_ts(to, ts + (e & 1) * kTileKeys + kk * 8,
+                   descriptor(v_lo + ((kStride * e * kKvBytes + kk * 2048) >> 4), hi), i > 0 || kk > 0);
+          commit(o_done);
+          commit(bars + kVEmpty + 8 * kStride * e);
+          // the scores of step i + 2 take the buffer whose weights this reads; the two products differ
+          // in shape, so only completion orders them (those of step i + 1 are there already)
+          if (i + 2 < n_mine) {
+            wait(o_done, (uint32_t)e & 1u);
+            scores((e + 2) % kMine, ring ^ (uint32_t)((e + 2) / kMine & 1));
+          }
+        }
       }
       if (!ok) {
         set_status(p.status, kStatusTimeout);
@@ -383,75 +395,57 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
-    // thread: dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of keys key0 + 32 u; the
+    // Two warps take every other step: a step's fixed costs (its barriers, and the proxy fence, which
+    // waits for the stores) are then paid once per 32 keys of a warp, and two steps overlap.
+    // thread: dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of keys key0 + 16 u; the
     // lanes of a quarter warp store to 8 different 16-byte banks (4 keys x 2 chunks of one block)
     const int c = (lane & 1) | (((lane >> 3) & 1) << 1);
-    const int key0 = ((lane >> 1) & 3) | ((lane >> 4) << 2) | ((warp & 3) << 3);
-    const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
+    const int key0 = ((lane >> 1) & 3) | ((lane >> 4) << 2) | ((warp & 1) << 3);
+    const uint32_t code_step = (uint32_t)p.heads * (kD / 2), scale_step = (uint32_t)p.heads * (kD / 16);
     struct Raw {
-      uint4 w[2];
-      uint32_t s[2];
+      uint4 w[4];
+      uint32_t s[4];
     };
-    auto fetch = [&](Raw& r, const Step& st, int64_t off_codes, int64_t off_scales) {
-      const int64_t slot = p.slots[st.seg];
-      const uint8_t* codes = p.base + off_codes + slot * p.slot_codes + (int64_t)h * (kD / 2) + 16 * c;
-      const uint8_t* scales = p.base + off_scales + slot * p.slot_scales + (int64_t)h * (kD / 16) + 2 * c;
+    const bool is_v = warp >= 12;
+    const uint32_t dst0 = smem_u32(is_v ? vbuf : kbuf) + (c >> 1) * kKvBlock + key0 * 128;
+    const uint32_t full = smem_u32(is_v ? ct.v_full : ct.k_full), empty = smem_u32(is_v ? ct.v_empty : ct.k_empty);
+    const uint8_t* codes0 = p.base + (is_v ? p.off_v_codes : p.off_k_codes) + (int64_t)h * (kD / 2) + 16 * c;
+    const uint8_t* scales0 = p.base + (is_v ? p.off_v_scales : p.off_k_scales) + (int64_t)h * (kD / 16) + 2 * c;
+    auto fetch = [&](Raw& r, const uint2 st) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // keys behind the step's last repeat it; their weights are 0
-        const int64_t key = st.t0 + min(key0 + 32 * u, st.n - 1);
-        r.w[u] = ldg_nc_v4(codes + key * code_step);
-        r.s[u] = ldg_nc_u16(scales + key * scale_step);
+      for (int u = 0; u < 4; ++u) {  // keys behind the step's last repeat it; their weights are 0
+        const uint32_t row = st.x + (uint32_t)min(key0 + 16 * u, (int)(st.y & 0xFFu) - 1);
+        r.w[u] = ldg_nc_v4(codes0 + (uint64_t)row * code_step);
+        r.s[u] = ldg_nc_u16(scales0 + (uint64_t)row * scale_step);
       }
     };
-    const uint32_t dst0 = (c >> 1) * kKvBlock + key0 * 128;
-    const uint32_t kdst = smem_u32(kbuf) + dst0, vdst = smem_u32(vbuf) + dst0;
-    auto decode = [&](const Raw& r, uint32_t dst) {
+    Raw raw;  // the next step of this pair, on its way since the last one was decoded
+    int j = (warp >> 1) & 1;
+    if (j < n) fetch(raw, list[j]);
+    bool ok = true;
+    for (; j < n; j += 2) {
+      const int b = j % kStages;
+      const uint2 next = list[min(j + 2, n - 1)];
+      ok = __all_sync(0xFFFFFFFFu,
+                      mbar_wait(empty + 8 * b, ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag, kWaitNs));
+      if (!ok) break;
+      const uint32_t dst = dst0 + b * kKvBytes;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t words[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
-        const uint32_t s2[2] = {e4m3_to_f16x2_bcast(r.s[u] & 0xFFu), e4m3_to_f16x2_bcast(r.s[u] >> 8)};
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t words[4] = {raw.w[u].x, raw.w[u].y, raw.w[u].z, raw.w[u].w};
+        const uint32_t s2[2] = {e4m3_to_f16x2_bcast(raw.s[u] & 0xFFu), e4m3_to_f16x2_bcast(raw.s[u] >> 8)};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t v[4];
           e2m1x8_times_scale(words[w], s2[w >> 1], v);
-          st_shared_v4(dst + u * (32 * 128) + (((4 * (c & 1) + w) ^ (key0 & 7)) << 4),
+          st_shared_v4(dst + u * (16 * 128) + (((4 * (c & 1) + w) ^ (key0 & 7)) << 4),
                        make_uint4(v[0], v[1], v[2], v[3]));
         }
       }
+      fetch(raw, next);
       fence_proxy_async_smem();
       __syncwarp();
-    };
-    // two steps' K and V on their way while one is decoded
-    Raw rk[2], rv[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (e < n) {
-        const Step st = read_step(p, list, e, first);
-        fetch(rk[e], st, p.off_k_codes, p.off_k_scales);
-        fetch(rv[e], st, p.off_v_codes, p.off_v_scales);
-      }
-    }
-    bool ok = true;
-    for (int j0 = 0; j0 < n && ok; j0 += 2) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int j = j0 + e;
-        if (j >= n || !ok) break;
-        const int b = j % kStages;
-        const uint32_t parity = ((uint32_t)(j / kStages) & 1u) ^ 1u;
-        Step st;
-        if (j + 2 < n) st = read_step(p, list, j + 2, first);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.k_empty[b]), parity, abort_flag, kWaitNs));
-        if (!ok) break;
-        decode(rk[e], kdst + b * kKvBytes);
-        if (lane == 0) mbar_arrive(smem_u32(&ct.k_full[b]));
-        if (j + 2 < n) fetch(rk[e], st, p.off_k_codes, p.off_k_scales);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.v_empty[b]), parity, abort_flag, kWaitNs));
-        if (!ok) break;
-        decode(rv[e], vdst + b * kKvBytes);
-        if (lane == 0) mbar_arrive(smem_u32(&ct.v_full[b]));
-        if (j + 2 < n) fetch(rv[e], st, p.off_v_codes, p.off_v_scales);
-      }
+      if (lane == 0) mbar_arrive(full + 8 * b);
     }
     if (!ok) {
       if (lane == 0) set_status(p.status, kStatusTimeout);
@@ -468,12 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     float mul = 0.0f, bias = 0.0f, lg = 0.0f, inv = 1.0f;
     bool vzero = false, ok = true;
     int seg_at = -1;
-    int64_t key_base = 0;
+    const bool idle = __all_sync(0xFFFFFFFFu, !live);  // no row of this warp's: its lanes of P and O are left as they are
     for (int i = 0; i < n_mine; ++i) {
-      const Step st = read_step(p, list, kPair ? i : 2 * i + tile, first);
-      if (st.seg != seg_at) {  // the slot's scales, and q . mu of this row
-        for (int e = seg_at < 0 ? 0 : seg_at; e < st.seg; ++e) key_base += p.tokens[e];
-        seg_at = st.seg;
+      if (idle) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ct.s_full[tile][i & 1]), (uint32_t)(i >> 1) & 1u, abort_flag,
+                                               kWaitNs))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive(smem_u32(&ct.p_ready[tile][i & 1]));
+        continue;
+      }
+      const uint2 st = list[kPair ? i : 2 * i + tile];
+      const int st_n = (int)(st.y & 0xFFu);
+      const bool full = st.y >> 16;
+      if ((int)(st.y >> 8 & 0xFFu) != seg_at) {  // the slot's scales, and q . mu of this row
+        seg_at = (int)(st.y >> 8 & 0xFFu);
         const SlotView sv = ct.view[seg_at];
         lg = sv.lg, inv = sv.inv, vzero = sv.vzero;
         const float4* mu = reinterpret_cast<const float4*>(
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       ld_tie(s);
       ld_tie(s + 32);
       float top, scale = mul, shift = bias;
-      if (st.full && !kExtras) {
+      if (full && !kExtras) {
         float t0 = s[0], t1 = s[1];
 #pragma unroll
         for (int e = 2; e + 3 < kTileKeys; e += 4) {
@@ -522,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         top = fmaf(fmaxf(fmaxf(t0, t1), fmaxf(s[kTileKeys - 2], s[kTileKeys - 1])), mul, bias);
       } else {
         // cap, bias and mask: raw products to log2 units, with -inf where the row does not see the key
-        const int kp0 = p.pos[st.seg] + st.t0;
+        const int t0 = (int)(st.x - (uint32_t)((int64_t)p.slots[seg_at] * p.chunk));
+        const int kp0 = p.pos[seg_at] + t0;
 #pragma unroll
         for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(s[e], mul, bias);
         if (kExtras && p.cap > 0.0f) {
@@ -535,18 +540,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 #pragma unroll
           for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(-slope, fabsf(d0 - (float)e), s[e]);
         }
-        if (!st.full) {
+        if (!full) {
           // visible: keys [lo, hi) of the step, and those below pre
-          int lo = 0, hi = st.n, pre = 0;
+          int lo = 0, hi = st_n, pre = 0;
           if (p.causal) hi = (int)min((int64_t)hi, (int64_t)qpos - kp0 + 1);
           if (p.window) lo = (int)max((int64_t)0, (int64_t)qpos - kp0 - p.window + 1);
-          if (p.prefix > kp0) pre = min(p.prefix - kp0, st.n);
+          if (p.prefix > kp0) pre = min(p.prefix - kp0, st_n);
+          const int32_t* docs = p.k_doc;
+          if (kExtras && docs) {
+            for (int e = 0; e < seg_at; ++e) docs += p.tokens[e];
+            docs += t0;
+          }
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             auto below = [&](int c) { c -= 32 * w; return c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u; };
             uint32_t see = (below(hi) & ~below(lo)) | below(pre);
-            if (kExtras && p.k_doc) {
-              const int doc = p.k_doc[key_base + st.t0 + min(32 * w + lane, st.n - 1)];
+            if (kExtras && docs) {
+              const int doc = docs[min(32 * w + lane, st_n - 1)];
               const int row0 = __shfl_sync(0xFFFFFFFFu, qdoc, 0);
               if (__all_sync(0xFFFFFFFFu, qdoc == row0)) {  // the warp's rows are of one document
                 see &= __ballot_sync(0xFFFFFFFFu, doc == row0);
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }

@@ -36,7 +36,7 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
 // Read-only 2-byte load that stays where it is written: issued ahead of its use on purpose.
 __device__ __forceinline__ uint32_t ldg_nc_u16(const void* p) {
   uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
     __syncthreads();
   }
   if (tree_part) {
-    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, r0, r0 + kRows, kWarps);
+    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, r0 + warp, r0 + kRows, kWarps);
     return;
   }
   if (threadIdx.x < kRows) {

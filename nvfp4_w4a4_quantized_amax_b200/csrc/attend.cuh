@@ -173,14 +173,15 @@ __device__ __forceinline__ int row_position(const Params& p, const int32_t* pare
   return pos;
 }
 
-// The drafts that rows [r0, r1) of cache head h see: themselves and their ancestors, one warp a
-// row, a lane holding 4 dims, in FP32.  A draft that a row does not see is never read for it, so
-// whatever it holds (NaN, Inf) cannot reach the row.  list: kMaxTreeDrafts entries of this warp.
-__device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parents, int16_t* list, int h, int64_t r0,
-                                          int64_t r1, int warps) {
+// The drafts that rows first, first + stride, ... below r1 of cache head h see: themselves and their
+// ancestors, for this warp, a lane holding 4 dims, in FP32.  A draft that a row does not see is
+// never read for it, so whatever it holds (NaN, Inf) cannot reach the row.  list: kMaxTreeDrafts
+// entries of this warp.
+__device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parents, int16_t* list, int h,
+                                          int64_t first, int64_t r1, int stride) {
   const int lane = threadIdx.x & 31;
   const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-  for (int64_t r = r0 + (threadIdx.x >> 5); r < r1 && r < p.rows; r += warps) {
+  for (int64_t r = first; r < r1 && r < p.rows; r += stride) {
     const int i = (int)(r / p.group);
     const int head = h * p.group + (int)(r - (int64_t)i * p.group);
     int n = 0;

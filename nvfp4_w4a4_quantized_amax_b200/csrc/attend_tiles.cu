@@ -53,14 +53,18 @@ struct Control {
   uint32_t tmem;
   volatile int abort;
   int32_t listed;
-  int32_t q_first, q_last, d_first, d_last;
+  int32_t q_first, q_last;
+  int32_t row_doc[256];
   SlotView view[kMaxWindowSlots];
   float m[128], l[128];  // of tile 1, when the two are joined
 };
 constexpr int kControlBytes = (sizeof(Control) + 127) / 128 * 128;
 
+// parents and, for the two warps that follow them, lists of ancestors
+constexpr int kTreeBytes = kMaxTreeDrafts * 4 + 2 * kMaxTreeDrafts * 2;
+
 constexpr int smem_bytes(bool pair) {
-  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 8;
+  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 8 + kTreeBytes;
 }
 
 // Instruction descriptor: D FP32 (bits 4..5 = 1), A and B binary16 (0), N >> 3, M >> 4; bit 16: B
@@ -157,21 +161,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   const int part = blockIdx.x, h = blockIdx.y;
   const int64_t r0 = (int64_t)blockIdx.z * (kPair ? 256 : 128);
   const int64_t r_end = min(r0 + (kPair ? 256 : 128), p.rows);
-  const bool tree_part = p.parents && part == p.parts - 1;
   const bool positions = p.causal || p.window || p.prefix || p.slopes;
 
-  // the drafts' parents and the lists of tree_rows take the key buffers, which are free till then
-  int32_t* parents = reinterpret_cast<int32_t*>(kbuf);
-  int16_t* ancestors = reinterpret_cast<int16_t*>(kbuf + kMaxTreeDrafts * 4) + warp * kMaxTreeDrafts;
-  static_assert(kMaxTreeDrafts * (4 + 2 * (kThreads / 32)) <= kStages * kKvBytes, "lists of tree_rows");
   pdl_wait();
-  if (p.parents && (tree_part || positions)) {
+  int32_t* parents = reinterpret_cast<int32_t*>(list + kMaxListed);
+  if (p.parents) {
     for (int i = threadIdx.x; i < p.drafts; i += kThreads) parents[i] = p.parents[i];
     __syncthreads();
-  }
-  if (tree_part) {
-    tree_rows(p, parents, ancestors, h, r0, r_end, kThreads / 32);
-    return;
   }
 
   const bool two = kPair && r_end - r0 > 128;  // the second tile of a pair has rows
@@ -191,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       mbar_init(smem_u32(&ct.done[t]), 1);
     }
     ct.abort = 0;
-    ct.q_first = ct.d_first = 0x7FFFFFFF;
-    ct.q_last = ct.d_last = -0x7FFFFFFF - 1;
+    ct.q_first = 0x7FFFFFFF;
+    ct.q_last = -0x7FFFFFFF - 1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -219,13 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     if (kExtras && p.slopes) slope = p.slopes[head] * kLog2e;
     if (kPair || tile == 0) {
       const int lo = __reduce_min_sync(0xFFFFFFFFu, qpos), hi = __reduce_max_sync(0xFFFFFFFFu, qpos);
-      const int dlo = __reduce_min_sync(0xFFFFFFFFu, qdoc), dhi = __reduce_max_sync(0xFFFFFFFFu, qdoc);
       if (lane == 0) {
         atomicMin(&ct.q_first, lo);
         atomicMax(&ct.q_last, hi);
-        atomicMin(&ct.d_first, dlo);
-        atomicMax(&ct.d_last, dhi);
       }
+      if (kExtras) ct.row_doc[threadIdx.x] = qdoc;
     }
     const uint8_t* src = p.q + i * p.q_pitch + (int64_t)head * kD * 2;
     unsigned top = 0;
@@ -294,10 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
       hi = __reduce_max_sync(0xFFFFFFFFu, hi);
       __syncwarp();
-      if (lane == 0) {
-        if (lo > ct.d_last || hi < ct.d_first) flags[rel] = 0;
-        else if (lo != hi || ct.d_first != ct.d_last) flags[rel] = 1;
+      bool some = false, every = lo == hi;  // rows with a document among them; rows of just that one
+      for (int r = lane; r < (kPair ? 256 : 128); r += 32) {
+        const int d = ct.row_doc[r];
+        some |= d >= lo && d <= hi;
+        every &= d == lo;
       }
+      some = __any_sync(0xFFFFFFFFu, some);
+      every = __all_sync(0xFFFFFFFFu, every);
+      if (lane == 0) flags[rel] = !some ? 0 : every ? flags[rel] : 1;
     }
     __syncthreads();
   }
@@ -391,6 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       }
       commit(smem_u32(&ct.done[t]));
       mbar_wait_drain(smem_u32(&ct.done[t]), 0, kWaitNs);
+    }
+    // the issuing warps' neighbours take the drafts that the rows see among themselves, each CTA of
+    // the window's split its share of the rows
+    if (p.parents && t >= 2) {
+      int16_t* ancestors = reinterpret_cast<int16_t*>(parents + kMaxTreeDrafts) + (t - 2) * kMaxTreeDrafts;
+      tree_rows(p, parents, ancestors, h, r0 + 2 * part + (t - 2), r_end, 2 * p.splits);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
@@ -739,7 +744,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     ready[dev].store(true, std::memory_order_relaxed);
   }
   const int64_t group = (kPair ? 2 : 1) * kTileRows;
-  return launch_pdl(attend_tiles_kernel<kExtras, kPair>, dim3(p.parts, p.heads, (unsigned)((p.rows + group - 1) / group)),
+  return launch_pdl(attend_tiles_kernel<kExtras, kPair>, dim3(p.splits, p.heads, (unsigned)((p.rows + group - 1) / group)),
                     kThreads, smem_bytes(kPair), s, p);
 }
 

@@ -63,6 +63,7 @@ struct Shared {
   SlotView view[kMaxWindowSlots];
   float m[kWarps][kRows], l[kWarps][kRows];
   int32_t row_pos[kRows], row_doc[kRows];
+  float gv_top;
 };
 
 __device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
@@ -114,11 +115,13 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   }
   if (threadIdx.x < kRows) {
     const int64_t r = r0 + threadIdx.x < p.rows ? r0 + threadIdx.x : p.rows - 1;
-    const int64_t i = r / p.group;
+    const int64_t i = p.by_group.div((uint32_t)r);
     sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
     if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[i] : 0;
   }
-  const float gv_top = load_slots(p, sh.view, part == 0 && h == 0 && r0 == 0);  // synchronises the CTA
+  if (warp == kWarps - 1) load_slots(p, sh.view, &sh.gv_top, part == 0 && h == 0 && r0 == 0);
+  __syncthreads();
+  const float gv_top = sh.gv_top;
   int q_first = sh.row_pos[0], q_last = q_first;
 #pragma unroll
   for (int i = 1; i < kRows; ++i) {
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   for (int u = 0; u < 2; ++u) {
     const int64_t r = r0 + g + 8 * u;
     const int64_t rr = r < p.rows ? r : p.rows - 1;
-    const int64_t i = rr / p.group;
+    const int64_t i = p.by_group.div((uint32_t)rr);
     const int head = h * p.group + (int)(rr - i * p.group);
     const uint8_t* src = p.q + i * p.q_pitch + ((int64_t)head * kD + 32 * c) * 2;
     uint32_t w[16];
@@ -150,13 +153,9 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
     top = max(top >> 16, top & 0xFFFFu);
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    // power of two that takes the row's largest element to [2^14, 2^15); a row of zeros, NaN or
-    // Inf (which then reaches the output) keeps 1, and so do exponents out of FP32's range
-    int e = 141 - (int)(top >> 7);
-    if (top == 0 || top >= 0x7F80u) e = 0;
-    e = e > 120 ? 120 : e;
-    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    fac[u] = p.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+    const int e = query_exponent(top);
+    const float up = exp2i(e);
+    fac[u] = p.scale * exp2i(-e);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       qa[ks][u] = pack_f16x2(bf16_lo(w[2 * ks]) * up, bf16_hi(w[2 * ks]) * up);
@@ -415,10 +414,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = (int64_t)p.heads * p.rows;
-  const int64_t row = (int64_t)blockIdx.x * (8 / kSplit) + warp / kSplit;
+  const int h = blockIdx.y;
+  const int64_t r = (int64_t)blockIdx.x * (8 / kSplit) + warp / kSplit;
   const int w = warp % kSplit;
-  const bool live = row < n;
-  const int64_t rr = live ? row : n - 1;
+  const bool live = r < p.rows;
+  const int64_t rr = h * p.rows + (live ? r : p.rows - 1);
   float top = -INFINITY;
   for (int i = lane; i < p.parts; i += 32) {
     const float l = p.part_l[i * n + rr];
@@ -466,8 +466,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   }
   if (!live) return;
   const float f = top == -INFINITY ? 0.0f : 1.0f / sum;
-  const int h = (int)(row / p.rows);
-  const int64_t r = row - (int64_t)h * p.rows, i = r / p.group;
+  const int64_t i = p.by_group.div((uint32_t)r);
   const int head = h * p.group + (int)(r - i * p.group);
   stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + 4 * lane) * 2,
          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f)));
@@ -558,6 +557,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.chunk = c.chunk_tokens;
   p.heads = c.heads;
   p.group = a.q_heads / c.heads;
+  p.by_group = FastDiv((uint32_t)p.group);
   p.n_slots = a.n_slots;
   p.rows = a.tq * p.group;
   const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows);
@@ -604,10 +604,9 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   else if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_rows<true>(p, grid, s);
   else e = launch_rows<false>(p, grid, s);
   if (e != cudaSuccess || p.parts == 1) return e;
-  const int64_t n = (int64_t)p.heads * p.rows;
   // few parts: a warp a row; more: eight warps share a row's
-  if (p.parts <= 8) return launch_pdl(attend_join_kernel<1>, dim3((unsigned)((n + 7) / 8)), 256, 0, s, p);
-  return launch_pdl(attend_join_kernel<8>, dim3((unsigned)n), 256, 0, s, p);
+  if (p.parts <= 8) return launch_pdl(attend_join_kernel<1>, dim3((unsigned)((p.rows + 7) / 8), p.heads), 256, 0, s, p);
+  return launch_pdl(attend_join_kernel<8>, dim3((unsigned)p.rows, p.heads), 256, 0, s, p);
 }
 
 }  // namespace nvfp4

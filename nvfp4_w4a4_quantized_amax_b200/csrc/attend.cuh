@@ -32,6 +32,7 @@ struct Params {
   int64_t slot_codes, slot_scales;
   int64_t chunk;  // tokens of a slot
   int32_t heads, group;  // cache heads, query heads of each
+  FastDiv by_group;
   int32_t n_slots;
   int32_t slots[kMaxWindowSlots];
   int32_t tokens[kMaxWindowSlots];
@@ -75,32 +76,54 @@ struct SlotView {
   int vzero;   // its values count as zero: g_V is 0 or under 2^-60 of the largest
 };
 
-// Reads the listed slots' scales (whole CTA); returns the largest g_V, 1 where all are 0.
-__device__ __forceinline__ float load_slots(const Params& p, SlotView* view, bool report) {
-  const float* gs = reinterpret_cast<const float*>(p.base + p.off_gscale);
-  for (int i = threadIdx.x; i < p.n_slots; i += blockDim.x) {
-    const bool ok = reinterpret_cast<const int32_t*>(p.base + p.off_tokens)[p.slots[i]] == p.tokens[i];
-    view[i].ok = ok;
-    view[i].gk = gs[2 * p.slots[i]];
-    view[i].lg = gs[2 * p.slots[i] + 1];  // g_V for now
-    if (!ok && report) set_status(p.status, kStatusShape);
+// Reads the listed slots' scales, one warp; *top_out = the largest g_V, 1 where all are 0.  The
+// caller synchronises before it uses either.
+__device__ __forceinline__ void load_slots(const Params& p, SlotView* view, float* top_out, bool report) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* tokens = reinterpret_cast<const int32_t*>(p.base + p.off_tokens);
+  const float2* gs = reinterpret_cast<const float2*>(p.base + p.off_gscale);
+  static_assert(kMaxWindowSlots <= 64, "two slots a lane");
+  int32_t held[2] = {0, 0};
+  float2 g[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (lane + 32 * u < p.n_slots) {
+      held[u] = tokens[p.slots[lane + 32 * u]];
+      g[u] = gs[p.slots[lane + 32 * u]];
+    }
   }
-  __syncthreads();
   float top = 0.0f;
-  for (int i = 0; i < p.n_slots; ++i)
-    if (view[i].ok) top = fmaxf(top, view[i].lg);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 32 * u < p.n_slots && held[u] == p.tokens[lane + 32 * u]) top = fmaxf(top, g[u].y);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
   if (!(top > 0.0f)) top = 1.0f;
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.n_slots; i += blockDim.x) {
-    const float r = view[i].lg / top;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = lane + 32 * u;
+    if (i >= p.n_slots) continue;
+    const bool ok = held[u] == p.tokens[i];
+    const float r = g[u].y / top;
     const bool zero = !(r > 8.6736173798840355e-19f);  // 2^-60
+    view[i].ok = ok;
+    view[i].gk = g[u].x;
     view[i].vzero = zero;
     view[i].lg = zero ? 0.0f : log2f(r);
     view[i].inv = zero ? 1.0f : 1.0f / r;
+    if (!ok && report) set_status(p.status, kStatusShape);
   }
-  __syncthreads();
-  return top;
+  if (lane == 0) *top_out = top;
 }
+
+// Exponent of the power of two that takes a row of queries with largest magnitude `top` (bf16 bits)
+// to [2^14, 2^15); 0 for a row of zeros, of NaN or Inf (which then reach the output).
+__device__ __forceinline__ int query_exponent(unsigned top) {
+  if (top == 0 || top >= 0x7F80u) return 0;
+  const int e = 141 - (int)(top >> 7);
+  return e > 120 ? 120 : e;  // 2^e and 2^-e stay FP32 numbers
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -158,7 +181,7 @@ __device__ __forceinline__ void store_row(const Params& p, int part, int h, int6
     if (with_l) p.part_l[at] = log2l;
     return;
   }
-  const int64_t i = r / p.group;
+  const int64_t i = p.by_group.div((uint32_t)r);
   const int head = h * p.group + (int)(r - i * p.group);
   stg_v2(p.o + i * p.o_pitch + ((int64_t)head * kD + d) * 2, make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)));
   if (with_l && p.lse) p.lse[(int64_t)head * p.tq + i] = log2l * kLn2;
@@ -166,7 +189,7 @@ __device__ __forceinline__ void store_row(const Params& p, int part, int h, int6
 
 // Position of row r's query.
 __device__ __forceinline__ int row_position(const Params& p, const int32_t* parents, int64_t r) {
-  const int64_t i = r / p.group;
+  const int64_t i = p.by_group.div((uint32_t)r);
   if (!p.parents) return p.q_pos ? p.q_pos[i] : p.q_pos0 + (int)i;
   int pos = p.q_pos0;
   for (int j = parent_of(p, parents, (int)i); j >= 0; j = parent_of(p, parents, j)) ++pos;
@@ -182,7 +205,7 @@ __device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parent
   const int lane = threadIdx.x & 31;
   const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
   for (int64_t r = first; r < r1 && r < p.rows; r += stride) {
-    const int i = (int)(r / p.group);
+    const int i = (int)(p.by_group.div((uint32_t)r));
     const int head = h * p.group + (int)(r - (int64_t)i * p.group);
     int n = 0;
     if (lane == 0)

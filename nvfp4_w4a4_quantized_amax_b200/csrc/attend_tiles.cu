@@ -54,7 +54,9 @@ struct Control {
   volatile int abort;
   int32_t listed;
   int32_t q_first, q_last;
+  float gv_top;
   int32_t row_doc[256];
+  float row_fac[256];  // factor of a row's products: scale and the power of two of its queries
   SlotView view[kMaxWindowSlots];
   float m[128], l[128];  // of tile 1, when the two are joined
 };
@@ -197,22 +199,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const float gv_top = load_slots(p, ct.view, part == 0 && h == 0 && blockIdx.z == 0);  // synchronises the CTA
-
-  // this thread's row (threads 0..255; the row's last for those behind the end): position,
-  // document, and the query in binary16, scaled by a power of two, into the swizzled operand tile
+  __syncthreads();
+  // this thread's row (threads 0..255; the last row for those behind the end): position, document
   const int tile = (warp >> 2) & 1;
   const int64_t row = r0 + (kPair ? tile * 128 : 0) + (threadIdx.x & 127);
   const bool live = warp < 8 && row < r_end;
   int qpos = 0, qdoc = 0;
-  float fac = 0.0f, slope = 0.0f;
+  float slope = 0.0f;
   if (warp < 8) {
     const int64_t rr = row < r_end ? row : r_end - 1;
-    const int64_t i = rr / p.group;
-    const int head = h * p.group + (int)(rr - i * p.group);
+    const int64_t i = p.by_group.div((uint32_t)rr);
     if (positions) qpos = row_position(p, parents, rr);
     if (kExtras && p.q_doc) qdoc = p.q_doc[i];
-    if (kExtras && p.slopes) slope = p.slopes[head] * kLog2e;
+    if (kExtras && p.slopes) slope = p.slopes[h * p.group + (int)(rr - i * p.group)] * kLog2e;
     if (kPair || tile == 0) {
       const int lo = __reduce_min_sync(0xFFFFFFFFu, qpos), hi = __reduce_max_sync(0xFFFFFFFFu, qpos);
       if (lane == 0) {
@@ -221,38 +220,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       }
       if (kExtras) ct.row_doc[threadIdx.x] = qdoc;
     }
-    const uint8_t* src = p.q + i * p.q_pitch + (int64_t)head * kD * 2;
-    unsigned top = 0;
-#pragma unroll 8
-    for (int k = 0; k < 16; ++k) {
-      const uint4 v = ldg_nc_v4_l1(src + 16 * k);
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                   __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  // the slots' scales by one warp, the queries by the others: half a warp a row, to binary16 scaled
+  // by a power of two, into the swizzled operand tiles (zeros behind the last row)
+  if (warp == kThreads / 32 - 1) {
+    load_slots(p, ct.view, &ct.gv_top, part == 0 && h == 0 && blockIdx.z == 0);
+  } else {
+    constexpr int kQWarps = kThreads / 32 - 1, kRounds = ((kPair ? 128 : 64) + kQWarps - 1) / kQWarps;
+    const int k = lane & 15;
+    uint4 v[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {  // every read on its way before the first is used
+      const int r = 2 * (warp + u * kQWarps) + (lane >> 4);
+      const int64_t rr = r0 + r < r_end ? r0 + r : r_end - 1;
+      const int64_t i = p.by_group.div((uint32_t)rr);
+      const int head = h * p.group + (int)(rr - i * p.group);
+      v[u] = ldg_nc_v4(p.q + i * p.q_pitch + (int64_t)head * kD * 2 + 16 * k);
     }
-    top = max(top >> 16, top & 0xFFFFu);
-    int e = 141 - (int)(top >> 7);
-    if (top == 0 || top >= 0x7F80u) e = 0;
-    e = e > 120 ? 120 : e;
-    // a negative scale goes into the queries, so that larger products are larger scores
-    const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), p.scale);
-    fac = fabsf(p.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
-    if (kPair || tile == 0) {
-      const int r = threadIdx.x & 127;
-      uint8_t* dst = qbuf + (kPair ? tile : 0) * kQBytes + r * 128;
-#pragma unroll 8
-      for (int k = 0; k < 16; ++k) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) {
-          v = ldg_nc_v4_l1(src + 16 * k);
-          v = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                         pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
-        }
-        *reinterpret_cast<uint4*>(dst + (k >> 3) * kQBlock + (((k & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int r = 2 * (warp + u * kQWarps) + (lane >> 4);
+      unsigned top = __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                              __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
+      top = max(top >> 16, top & 0xFFFFu);
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+      if (r >= (kPair ? 256 : 128)) continue;
+      const int e = query_exponent(top);
+      const bool some = r0 + r < r_end;
+      // a negative scale goes into the queries, so that larger products are larger scores
+      const float up = copysignf(exp2i(e), p.scale);
+      const uint4 w = make_uint4(pack_f16x2(bf16_lo(v[u].x) * up, bf16_hi(v[u].x) * up),
+                                 pack_f16x2(bf16_lo(v[u].y) * up, bf16_hi(v[u].y) * up),
+                                 pack_f16x2(bf16_lo(v[u].z) * up, bf16_hi(v[u].z) * up),
+                                 pack_f16x2(bf16_lo(v[u].w) * up, bf16_hi(v[u].w) * up));
+      *reinterpret_cast<uint4*>(qbuf + (r >> 7) * kQBytes + (k >> 3) * kQBlock + (r & 127) * 128 +
+                                (((k & 7) ^ (r & 7)) << 4)) = some ? w : make_uint4(0, 0, 0, 0);
+      if (k == 0) ct.row_fac[r] = fabsf(p.scale) * exp2i(-e);
     }
+    fence_proxy_async_smem();
   }
   __syncthreads();
+  const float gv_top = ct.gv_top;
+  const float fac = ct.row_fac[(kPair ? tile * 128 : 0) + (threadIdx.x & 127)];
 
   // the key steps of this CTA's range that some row sees, in order
   const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);

@@ -12,7 +12,7 @@ namespace {
 
 using tc::smem_u32;
 
-constexpr int kRows = 16;       // query rows of a CTA: the M of one mma.sync
+constexpr int kRows = 16;       // most query rows of a cache head that a CTA takes
 constexpr int kStep = 32;       // keys a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -25,23 +25,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+// Transpose of the 8 x 8 matrix of 16-bit values that a warp holds, row lane / 4, columns
+// 2 (lane % 4) and + 1.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-  return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-}
-
 // A warp's ring of key steps on their way from the cache: codes, scales and what the step is.
-constexpr int kRing = 4;
+constexpr int kRing = 3;
 struct Stage {
   uint8_t k_codes[kStep * 64], v_codes[kStep * 64];
   uint8_t k_scales[kStep * 8], v_scales[kStep * 8];
@@ -53,7 +46,9 @@ struct StepInfo {
 struct Shared {
   union {
     Stage ring[kWarps][kRing];
-    float o[kWarps][kRows][kD];
+    struct {
+      float o[kWarps][kRows][kD], m[kWarps][kRows], l[kWarps][kRows];
+    } join;
     struct {
       int32_t parents[kMaxTreeDrafts];
       int16_t list[kWarps][kMaxTreeDrafts];
@@ -61,8 +56,8 @@ struct Shared {
   };
   StepInfo info[kWarps][kRing];
   SlotView view[kMaxWindowSlots];
-  float m[kWarps][kRows], l[kWarps][kRows];
   int32_t row_pos[kRows], row_doc[kRows];
+  float row_fac[kRows];
   float gv_top;
 };
 
@@ -78,23 +73,25 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Within an 8-key tile the product's column 2 c + e is key c + 4 e: the lanes of one read of V then
-// take neighbouring keys.
+// Key of the product's index n within 8: index 2 c + e is key c + 4 e, so that the lanes of one read
+// of V take neighbouring keys.
 __device__ __forceinline__ int tile_key(int n) { return (n >> 1) + 4 * (n & 1); }
 
-// One CTA: 16 query rows of one cache head against a range of the window's 32-key steps, the
-// steps dealt out to four warps.  mma.sync and not tcgen05: with at most 16 rows the kernel
+// One CTA: up to 8 kTiles query rows of one cache head against a range of the window's 32-key
+// steps, the steps dealt out to four warps.  mma.sync and not tcgen05: with so few rows the kernel
 // waits for the cache's bytes and for their decoding, and mma.sync takes the decoded codes from
-// registers, where tcgen05 would have them stored to shared memory first.
-// Each warp copies its steps' codes and scales into its own ring three steps ahead (cp.async: no
+// registers, where tcgen05 would have them stored to shared memory first.  Keys and dims are the
+// product's 16 rows and queries its 8 columns, S^T = K~ Q^T and O^T = V~^T P^T: a row of queries
+// alone then wastes 7 of 8 columns and not 15 of 16 rows, and O takes 32 registers a tile.
+// Each warp copies its steps' codes and scales into its own ring two steps ahead (cp.async: no
 // registers, and no barrier but the warp's own).
-// Lane (g, c) = (lane / 4, lane % 4).  Scores: the contraction runs over dims in an order in
-// which lane c owns dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of key g of an
-// 8-key tile.  Values: lane (g, c) owns dims 16 g .. 16 g + 15 (8 bytes, one scale) of keys
-// c, c + 4 of a tile; nibbles of the two keys are interleaved before the conversion, which
-// then yields the pairs of columns the product wants.
-template <bool kExtras>  // a cap, a bias or documents
-__global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_constant__ Params p) {
+// Lane (g, c) = (lane / 4, lane % 4).  K~: the contraction runs over dims in an order in which lane
+// c owns dims 32 c .. 32 c + 31 (16 bytes of codes, two scale bytes) of keys g and g + 8 of 16.
+// V~^T: lane (g, c) owns dims 16 g .. 16 g + 15 (8 bytes, one scale) of the keys of columns 2 c,
+// 2 c + 1 (and + 8); nibbles of two keys are interleaved before the conversion, which then yields
+// the pairs the product wants.  P^T comes from S^T by one 8 x 8 transpose a tile.
+template <bool kExtras, int kTiles>  // kExtras: a cap, a bias or documents
+__global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
   pdl_trigger();
@@ -102,7 +99,6 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int part = blockIdx.x, h = blockIdx.y;
-  constexpr int64_t r0 = 0;
   const bool tree_part = p.parents && part == p.parts - 1;
   const bool positions = p.causal || p.window || p.prefix || p.slopes;
   if (p.parents && (tree_part || positions)) {
@@ -110,37 +106,75 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
     __syncthreads();
   }
   if (tree_part) {
-    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, r0 + warp, r0 + kRows, kWarps);
+    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, warp, kRows, kWarps);
     return;
   }
-  if (threadIdx.x < kRows) {
-    const int64_t r = r0 + threadIdx.x < p.rows ? r0 + threadIdx.x : p.rows - 1;
-    const int64_t i = p.by_group.div((uint32_t)r);
-    sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
-    if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[i] : 0;
-  }
-  if (warp == kWarps - 1) load_slots(p, sh.view, &sh.gv_top, part == 0 && h == 0 && r0 == 0);
-  __syncthreads();
-  const float gv_top = sh.gv_top;
-  int q_first = sh.row_pos[0], q_last = q_first;
+  int q_first = 0, q_last = 0;
+  if (positions || (kExtras && p.q_doc)) {
+    if (threadIdx.x < kRows) {
+      const int r = (int)min((int64_t)threadIdx.x, p.rows - 1);
+      sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
+      if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[p.by_group.div((uint32_t)r)] : 0;
+    }
+    __syncthreads();  // and the ring's memory is free of the drafts' parents
+    q_first = q_last = sh.row_pos[0];
 #pragma unroll
-  for (int i = 1; i < kRows; ++i) {
-    q_first = min(q_first, sh.row_pos[i]);
-    q_last = max(q_last, sh.row_pos[i]);
+    for (int i = 1; i < kRows; ++i) {
+      q_first = min(q_first, sh.row_pos[i]);
+      q_last = max(q_last, sh.row_pos[i]);
+    }
   }
 
-  // this lane's rows: g and g + 8; queries as binary16 A fragments and each row's factor
-  uint32_t qa[8][4];
-  float fac[2];
-  int qpos[2], qdoc[2] = {0, 0};
-  float slope[2] = {0.0f, 0.0f};
+  const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
+  const uint32_t code_step = (uint32_t)p.heads * (kD / 2), scale_step = (uint32_t)p.heads * (kD / 16);
+  // next step that some row sees, into ring place `to`
+  int next = first + warp, next_seg = 0;
+  auto issue = [&](int to) {
+    StepInfo si = {0, 0, 0, 0};
+    for (; next < last; next += kWarps) {
+      while (next >= p.step_end[next_seg]) ++next_seg;
+      const int t0 = (next - (next_seg ? p.step_end[next_seg - 1] : 0)) * kStep;
+      const int n = min(kStep, p.tokens[next_seg] - t0);
+      const int kp0 = p.pos[next_seg] + t0;
+      const int vis = visibility(p, kp0, kp0 + n - 1, q_first, q_last);
+      if (vis == 0) continue;
+      si = {next_seg, t0, n, n < kStep || (kExtras && p.k_doc) ? 1 : vis};
+      next += kWarps;
+      break;
+    }
+    if (si.n > 0) {
+      Stage& st = sh.ring[warp][to];
+      const uint32_t row0 = (uint32_t)((int64_t)p.slots[si.seg] * p.chunk + si.t0);
+      const uint8_t* kc = p.base + p.off_k_codes + (int64_t)h * (kD / 2) + 16 * c;
+      const uint8_t* vc = p.base + p.off_v_codes + (int64_t)h * (kD / 2) + 16 * c;
+      const uint8_t* ks = p.base + p.off_k_scales + (int64_t)h * (kD / 16);
+      const uint8_t* vs = p.base + p.off_v_scales + (int64_t)h * (kD / 16);
+      const uint32_t kd = smem_u32(st.k_codes), vd = smem_u32(st.v_codes);
+      auto row = [&](int key) { return (uint64_t)(row0 + (uint32_t)min(key, si.n - 1)); };
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t r = r0 + g + 8 * u;
-    const int64_t rr = r < p.rows ? r : p.rows - 1;
-    const int64_t i = p.by_group.div((uint32_t)rr);
-    const int head = h * p.group + (int)(rr - i * p.group);
-    const uint8_t* src = p.q + i * p.q_pitch + ((int64_t)head * kD + 32 * c) * 2;
+      for (int t = 0; t < 4; ++t) {  // keys behind the step's last repeat it and are masked
+        copy_16(kd + (32 * t + lane) * 16, kc + row(8 * t + tile_key(g)) * code_step);
+        const int key = 8 * t + g;
+        copy_16(vd + key * 64 + ((c ^ (key & 2)) << 4), vc + row(key) * code_step);
+      }
+      copy_8(smem_u32(st.k_scales) + lane * 8, ks + row((lane & ~7) + tile_key(lane & 7)) * scale_step);
+      copy_8(smem_u32(st.v_scales) + lane * 8, vs + row(lane) * scale_step);
+    }
+    if (lane == 0) sh.info[warp][to] = si;
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
+  if (warp == kWarps - 1) load_slots(p, sh.view, &sh.gv_top, part == 0 && h == 0);
+
+  // queries as binary16 B fragments: lane (g, c) holds dims 32 c .. of row 8 tile + g
+  uint32_t qb[kTiles][8][2];
+#pragma unroll
+  for (int u = 0; u < kTiles; ++u) {
+    const int r = (int)min((int64_t)(8 * u + g), p.rows - 1);
+    const int i = (int)p.by_group.div((uint32_t)r);
+    const int head = h * p.group + (r - i * p.group);
+    const uint8_t* src = p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 32 * c) * 2;
     uint32_t w[16];
     unsigned top = 0;
 #pragma unroll
@@ -155,250 +189,258 @@ __global__ void __launch_bounds__(kThreads, 3) attend_rows_kernel(const __grid_c
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const int e = query_exponent(top);
     const float up = exp2i(e);
-    fac[u] = p.scale * exp2i(-e);
+    if (warp == 0 && c == 0) sh.row_fac[8 * u + g] = p.scale * exp2i(-e);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      qa[ks][u] = pack_f16x2(bf16_lo(w[2 * ks]) * up, bf16_hi(w[2 * ks]) * up);
-      qa[ks][2 + u] = pack_f16x2(bf16_lo(w[2 * ks + 1]) * up, bf16_hi(w[2 * ks + 1]) * up);
-    }
-    qpos[u] = sh.row_pos[g + 8 * u];
-    if (kExtras) {
-      qdoc[u] = sh.row_doc[g + 8 * u];
-      if (p.slopes) slope[u] = p.slopes[head] * kLog2e;
+      qb[u][ks][0] = pack_f16x2(bf16_lo(w[2 * ks]) * up, bf16_hi(w[2 * ks]) * up);
+      qb[u][ks][1] = pack_f16x2(bf16_lo(w[2 * ks + 1]) * up, bf16_hi(w[2 * ks + 1]) * up);
     }
   }
+  __syncthreads();
 
-  float o[16][4];
+  // statistics of this lane's rows: row 8 u + 2 c + e is [u][e]
+  float o[kTiles][8][4], m[kTiles][2], l[kTiles][2], bias[kTiles][2], mul[kTiles][2];
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int u = 0; u < kTiles; ++u) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-  const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
-  const int64_t code_step = (int64_t)p.heads * (kD / 2), scale_step = (int64_t)p.heads * (kD / 16);
-  // next step that some row sees, into ring place `to`
-  int next = first + warp, next_seg = 0;
-  auto issue = [&](int to) {
-    StepInfo si = {0, 0, 0, 0};
-    for (; next < last; next += kWarps) {
-      while (next >= p.step_end[next_seg]) ++next_seg;
-      if (!sh.view[next_seg].ok) continue;
-      const int t0 = (next - (next_seg ? p.step_end[next_seg - 1] : 0)) * kStep;
-      const int n = min(kStep, p.tokens[next_seg] - t0);
-      const int kp0 = p.pos[next_seg] + t0;
-      const int vis = visibility(p, kp0, kp0 + n - 1, q_first, q_last);
-      if (vis == 0) continue;
-      si = {next_seg, t0, n, n < kStep || (kExtras && p.k_doc) ? 1 : vis};
-      next += kWarps;
-      break;
-    }
-    if (si.n > 0) {
-      Stage& st = sh.ring[warp][to];
-      const int64_t slot = p.slots[si.seg], row0 = (int64_t)si.t0 * p.heads + h;
-      const uint8_t* kc = p.base + p.off_k_codes + slot * p.slot_codes + row0 * (kD / 2) + 16 * c;
-      const uint8_t* vc = p.base + p.off_v_codes + slot * p.slot_codes + row0 * (kD / 2) + 16 * c;
-      const uint8_t* ks = p.base + p.off_k_scales + slot * p.slot_scales + row0 * (kD / 16);
-      const uint8_t* vs = p.base + p.off_v_scales + slot * p.slot_scales + row0 * (kD / 16);
-      const uint32_t kd = smem_u32(st.k_codes), vd = smem_u32(st.v_codes);
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {  // keys behind the step's last repeat it and are masked
-        copy_16(kd + (32 * t + lane) * 16, kc + min(8 * t + tile_key(g), si.n - 1) * code_step);
-        const int key = 8 * t + g;
-        copy_16(vd + key * 64 + ((c ^ (key & 2)) << 4), vc + min(key, si.n - 1) * code_step);
-      }
-      copy_8(smem_u32(st.k_scales) + lane * 8, ks + min((lane & ~7) + tile_key(lane & 7), si.n - 1) * scale_step);
-      copy_8(smem_u32(st.v_scales) + lane * 8, vs + min(lane, si.n - 1) * scale_step);
-    }
-    if (lane == 0) sh.info[warp][to] = si;
-    copy_commit();
-  };
-  int seg_at = -1, key_seg = 0;
-  float bias[2] = {0.0f, 0.0f}, mul[2] = {0.0f, 0.0f}, lg = 0.0f, inv = 1.0f;
-  int64_t key_base = 0;  // keys listed before slot key_seg
+      for (int k = 0; k < 4; ++k) o[u][j][k] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m[u][e] = -INFINITY, l[u][e] = 0.0f, bias[u][e] = mul[u][e] = 0.0f;
+  }
+  int seg_at = -1;
+  float lg = 0.0f, inv = 1.0f;
   bool vzero = false;
-  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) issue(i);
-  for (int at = 0;; at = (at + 1) % kRing) {
+  for (int at = 0;; at = at + 1 == kRing ? 0 : at + 1) {
     copy_wait<kRing - 2>();
     __syncwarp();
     const StepInfo si = sh.info[warp][at];
     if (si.n == 0) break;
-    const int seg = si.seg, t0 = si.t0, n = si.n, vis = si.vis;
-    const int kp0 = p.pos[seg] + t0;
-    if (kExtras && p.k_doc)
-      for (; key_seg < seg; ++key_seg) key_base += p.tokens[key_seg];
     const Stage& stage = sh.ring[warp][at];
-    if (seg != seg_at) {  // the slot's scales and q . mu of this lane's rows
-      seg_at = seg;
-      const SlotView sv = sh.view[seg];
+    if (si.seg != seg_at) {  // the slot's scales, and q . mu of this lane's rows
+      seg_at = si.seg;
+      const SlotView sv = sh.view[seg_at];
       lg = sv.lg, inv = sv.inv, vzero = sv.vzero;
       const float4* mu = reinterpret_cast<const float4*>(
-          p.base + p.off_mu + (((int64_t)p.slots[seg] * p.heads + h) * kD + 32 * c) * 4);
-      float acc[2] = {0.0f, 0.0f};
+          p.base + p.off_mu + (((int64_t)p.slots[seg_at] * p.heads + h) * kD + 32 * c) * 4);
+      float acc[kTiles];
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) acc[u] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const float4 v = __ldg(mu + ks);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kTiles; ++u) {
           float x, y;
-          f16x2_to_f32x2(qa[ks][u], x, y);
+          f16x2_to_f32x2(qb[u][ks][0], x, y);
           acc[u] = fmaf(x, v.x, fmaf(y, v.y, acc[u]));
-          f16x2_to_f32x2(qa[ks][2 + u], x, y);
+          f16x2_to_f32x2(qb[u][ks][1], x, y);
           acc[u] = fmaf(x, v.z, fmaf(y, v.w, acc[u]));
         }
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float f = kExtras && p.cap > 0.0f ? fac[u] : fac[u] * kLog2e;  // log2 units without a cap
-        bias[u] = quad_sum(acc[u]) * f;
-        mul[u] = f * sv.gk;
-      }
-    }
-    // scores of 4 tiles of 8 keys
-    float s[4][4];
+      for (int u = 0; u < kTiles; ++u) {
+        acc[u] += __shfl_xor_sync(0xFFFFFFFFu, acc[u], 1);
+        acc[u] += __shfl_xor_sync(0xFFFFFFFFu, acc[u], 2);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[t][k] = 0.0f;
-      const uint4 kw = *reinterpret_cast<const uint4*>(stage.k_codes + (32 * t + lane) * 16);
-      const uint32_t kb = *reinterpret_cast<const uint16_t*>(stage.k_scales + (8 * t + g) * 8 + 2 * c);
-      const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
-      const uint32_t s2[2] = {e4m3_to_f16x2_bcast(kb & 0xFFu), e4m3_to_f16x2_bcast(kb >> 8)};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t b[4];
-        e2m1x8_times_scale(words[w], s2[w >> 1], b);
-        mma_f16(s[t], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2], qa[2 * w][3], b[0], b[1]);
-        mma_f16(s[t], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2], qa[2 * w + 1][3], b[2], b[3]);
-      }
-    }
-    // element k of a tile: row g + 8 (k / 2), key c + 4 (k % 2)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int u = k >> 1, key = 8 * t + c + 4 * (k & 1);
-        float x = fmaf(s[t][k], mul[u], bias[u]);
-        if (kExtras) {
-          if (p.cap > 0.0f) x = softcap(x, p.cap, rcap) * kLog2e;
-          if (p.slopes) x = fmaf(-slope[u], fabsf((float)(qpos[u] - (kp0 + key))), x);
-        }
-        if (vis == 1) {
-          bool see = key < n && visible(p, kp0 + key, qpos[u]);
-          if (kExtras && p.k_doc) see = see && p.k_doc[key_base + t0 + min(key, n - 1)] == qdoc[u];
-          if (!see) x = -INFINITY;
-        }
-        s[t][k] = x;
-      }
-    }
-    float alpha[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) top = fmaxf(top, fmaxf(s[t][2 * u], s[t][2 * u + 1]));
-      top = quad_max(top);
-      const float mn = fmaxf(m[u], top + lg);
-      alpha[u] = mn == -INFINITY ? 1.0f : ex2(m[u] - mn);
-      m[u] = mn;
-      const float ref = mn == -INFINITY ? 0.0f : mn - lg - kShift;  // a row that has seen nothing: weights 0
-      float sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int k = 2 * u; k < 2 * u + 2; ++k) {
-          s[t][k] = ex2(s[t][k] - ref);
-          sum += s[t][k];
+        for (int e = 0; e < 2; ++e) {
+          const float fac = sh.row_fac[8 * u + 2 * c + e];
+          const float f = kExtras && p.cap > 0.0f ? fac : fac * kLog2e;  // log2 units without a cap
+          bias[u][e] = __shfl_sync(0xFFFFFFFFu, acc[u], 4 * (2 * c + e)) * f;
+          mul[u][e] = f * sv.gk;
         }
       }
-      l[u] = fmaf(sum, inv, l[u] * alpha[u]);
     }
-    if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        o[j][0] *= alpha[0];
-        o[j][1] *= alpha[0];
-        o[j][2] *= alpha[1];
-        o[j][3] *= alpha[1];
-      }
-    }
-    if (!vzero) {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {  // 16 keys: tiles 2 ks and 2 ks + 1
-      const uint32_t a0 = pack_f16x2(s[2 * ks][0], s[2 * ks][1]), a1 = pack_f16x2(s[2 * ks][2], s[2 * ks][3]);
-      const uint32_t a2 = pack_f16x2(s[2 * ks + 1][0], s[2 * ks + 1][1]);
-      const uint32_t a3 = pack_f16x2(s[2 * ks + 1][2], s[2 * ks + 1][3]);
-      uint2 wa[2], wb[2];
-      uint32_t s2[2];
+    if (sh.view[seg_at].ok) {
+      // S^T: element k of [tile t][u] is key 16 t + 8 (k / 2) + tile_key(g), row 8 u + 2 c + k % 2
+      float s[2][kTiles][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = 16 * ks + 8 * t + c;  // and key + 4
-        const int off = (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1);
-        wa[t] = *reinterpret_cast<const uint2*>(stage.v_codes + key * 64 + off);
-        wb[t] = *reinterpret_cast<const uint2*>(stage.v_codes + (key + 4) * 64 + off);
-        const uint32_t pair = stage.v_scales[key * 8 + g] | ((uint32_t)stage.v_scales[(key + 4) * 8 + g] << 8);
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[t]) : "h"((uint16_t)pair));
-      }
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {  // 8 dims of the lane's block at a time
-        uint32_t even[2][4], odd[2][4];
+        for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t xa = w ? wa[t].y : wa[t].x, xb = w ? wb[t].y : wb[t].x;
-          e2m1x8_times_scale((xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u), s2[t], even[t]);
-          e2m1x8_times_scale(((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u), s2[t], odd[t]);
+          for (int k = 0; k < 4; ++k) s[t][u][k] = 0.0f;
+        uint4 kw[2];
+        uint32_t s2[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // keys g and g + 8
+          kw[e] = *reinterpret_cast<const uint4*>(stage.k_codes + (64 * t + 32 * e + lane) * 16);
+          const uint32_t kb = *reinterpret_cast<const uint16_t*>(stage.k_scales + (16 * t + 8 * e + g) * 8 + 2 * c);
+          s2[e][0] = e4m3_to_f16x2_bcast(kb & 0xFFu);
+          s2[e][1] = e4m3_to_f16x2_bcast(kb >> 8);
         }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            e2m1x8_times_scale(w == 0 ? kw[e].x : w == 1 ? kw[e].y : w == 2 ? kw[e].z : kw[e].w, s2[e][w >> 1], a[e]);
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u) {
+            mma_f16(s[t][u], a[0][0], a[1][0], a[0][1], a[1][1], qb[u][2 * w][0], qb[u][2 * w][1]);
+            mma_f16(s[t][u], a[0][2], a[1][2], a[0][3], a[1][3], qb[u][2 * w + 1][0], qb[u][2 * w + 1][1]);
+          }
+        }
+      }
+      const int kp0 = p.pos[seg_at] + si.t0;
+      bool grow = false;
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_f16(o[8 * w + 2 * k], a0, a1, a2, a3, even[0][k], even[1][k]);
-          mma_f16(o[8 * w + 2 * k + 1], a0, a1, a2, a3, odd[0][k], odd[1][k]);
+          const int e = k & 1;
+          const int rr = 8 * u + 2 * c + e;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            float x = fmaf(s[t][u][k], mul[u][e], bias[u][e]);
+            if (kExtras || si.vis == 1) {
+              const int key = 16 * t + 8 * (k >> 1) + tile_key(g);
+              const int qpos = positions ? sh.row_pos[rr] : 0;
+              if (kExtras) {
+                if (p.cap > 0.0f) x = softcap(x, p.cap * kLog2e, 2.0f * kLog2e / p.cap);
+                if (p.slopes) {
+                  const int r = (int)min((int64_t)rr, p.rows - 1);
+                  const float slope = p.slopes[h * p.group + (r - (int)p.by_group.div((uint32_t)r) * p.group)];
+                  x = fmaf(-slope * kLog2e, fabsf((float)(qpos - (kp0 + key))), x);
+                }
+              }
+              if (si.vis == 1) {
+                bool see = key < si.n && visible(p, kp0 + key, qpos);
+                if (kExtras && p.k_doc) {
+                  const int32_t* docs = p.k_doc;
+                  for (int i = 0; i < seg_at; ++i) docs += p.tokens[i];
+                  see = see && docs[si.t0 + min(key, si.n - 1)] == sh.row_doc[rr];
+                }
+                if (!see) x = -INFINITY;
+              }
+            }
+            s[t][u][k] = x;
+            grow |= x + lg > m[u][e] + kLazy || (m[u][e] == -INFINITY && x > -INFINITY);
+          }
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {  // new maxima: the same in every lane of a row
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(s[0][u][e], s[0][u][2 + e]), fmaxf(s[1][u][e], s[1][u][2 + e]));
+#pragma unroll
+            for (int x = 16; x > 2; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+            const float mn = fmaxf(m[u][e], top + lg);
+            const float alpha = mn == -INFINITY ? 1.0f : ex2(m[u][e] - mn);
+            m[u][e] = mn;
+            l[u][e] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              o[u][j][e] *= alpha;
+              o[u][j][2 + e] *= alpha;
+            }
+          }
+        }
+      }
+      // weights, transposed: columns 2 c, 2 c + 1 of 16 keys of row g
+      uint32_t pb[2][kTiles][2];
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        float ref[2], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[e] = m[u][e] == -INFINITY ? 0.0f : m[u][e] - lg - kUp;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float w0 = ex2(s[t][u][2 * half] - ref[0]), w1 = ex2(s[t][u][2 * half + 1] - ref[1]);
+            sum[0] += w0;
+            sum[1] += w1;
+            pb[t][u][half] = transpose_8x8(pack_f16x2(w0, w1));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[u][e] = fmaf(sum[e], inv, l[u][e]);
+      }
+      if (!vzero) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint2 wa[2], wb[2];
+          uint32_t s2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // keys of columns 2 c, 2 c + 1, and of 8 further
+            const int key = 16 * t + 8 * e + c;  // and key + 4
+            const int off = (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1);
+            wa[e] = *reinterpret_cast<const uint2*>(stage.v_codes + key * 64 + off);
+            wb[e] = *reinterpret_cast<const uint2*>(stage.v_codes + (key + 4) * 64 + off);
+            const uint32_t pair = stage.v_scales[key * 8 + g] | ((uint32_t)stage.v_scales[(key + 4) * 8 + g] << 8);
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[e]) : "h"((uint16_t)pair));
+          }
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {  // even, then odd dims of the lane's block
+            uint32_t a[2][2][4];  // [column pair][8 dims of the block][dim / 2]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t xa = w ? wa[e].y : wa[e].x, xb = w ? wb[e].y : wb[e].x;
+                const uint32_t both = odd ? ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u)
+                                          : (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
+                e2m1x8_times_scale(both, s2[e], a[e][w]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int u = 0; u < kTiles; ++u)
+                mma_f16(o[u][2 * k + odd], a[0][0][k], a[0][1][k], a[1][0][k], a[1][1][k], pb[t][u][0], pb[t][u][1]);
+          }
         }
       }
     }
-    }
     __syncwarp();
-    issue((at + kRing - 1) % kRing);
+    issue(at == 0 ? kRing - 1 : at - 1);
   }
   copy_wait<0>();
 
-  // join the warps: element k of o[j]: row g + 8 (k / 2), dim 32 c + 16 (k % 2) + j
+  // join the warps: element k of o[u][j] is dim 16 g + 8 (k / 2) + j of row 8 u + 2 c + k % 2
   __syncthreads();  // the rings share this memory
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float ls = quad_sum(l[u]);
-    if (c == 0) {
-      sh.m[warp][g + 8 * u] = m[u];
-      sh.l[warp][g + 8 * u] = ls;
+  for (int u = 0; u < kTiles; ++u) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 16; x > 2; x >>= 1) l[u][e] += __shfl_xor_sync(0xFFFFFFFFu, l[u][e], x);
+      if (g == 0) {
+        sh.join.m[warp][8 * u + 2 * c + e] = m[u][e];
+        sh.join.l[warp][8 * u + 2 * c + e] = l[u][e];
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; j += 4)
+        *reinterpret_cast<float4*>(&sh.join.o[warp][8 * u + 2 * c + (k & 1)][16 * g + 8 * (k >> 1) + j]) =
+            make_float4(o[u][j][k], o[u][j + 1][k], o[u][j + 2][k], o[u][j + 3][k]);
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int j = 0; j < 16; j += 4)
-      *reinterpret_cast<float4*>(&sh.o[warp][g + 8 * (k >> 1)][32 * c + 16 * (k & 1) + j]) =
-          make_float4(o[j][k], o[j + 1][k], o[j + 2][k], o[j + 3][k]);
   __syncthreads();
-  for (int r = warp; r < kRows && r0 + r < p.rows; r += kWarps) {
+  for (int r = warp; r < 8 * kTiles && r < p.rows; r += kWarps) {
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.join.m[w][r]);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (sh.l[w][r] == 0.0f) continue;  // saw nothing
-      const float f = ex2(sh.m[w][r] - top);
-      sum = fmaf(f, sh.l[w][r], sum);
-      const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][r][4 * lane]);
+      if (sh.join.l[w][r] == 0.0f) continue;  // saw nothing
+      const float f = ex2(sh.join.m[w][r] - top);
+      sum = fmaf(f, sh.join.l[w][r], sum);
+      const float4 v = *reinterpret_cast<const float4*>(&sh.join.o[w][r][4 * lane]);
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum * gv_top;
-    store_row(p, part, h, r0 + r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
-              sum == 0.0f ? -INFINITY : top + log2f(sum) - kShift, lane == 0);
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum * sh.gv_top;
+    store_row(p, part, h, r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
+              sum == 0.0f ? -INFINITY : top + log2f(sum) - kUp, lane == 0);
   }
 }
 
@@ -483,10 +525,11 @@ struct Plan {
   int32_t splits;       // CTAs that share a window
 };
 
-// Up to 16 rows a cache head: 16-row CTAs, about three an SM, each with two steps a warp at least.
+// Up to 16 rows a cache head: CTAs of 8 or 16 rows, as many as run at once (a tree's own part among
+// them), each with two steps a warp at least.
 // More: tiles of 128 rows; the keys are split where rows and heads do not fill the SMs evenly, by
 // the least of waves * (steps a CTA + a CTA's own cost), with the partial results' traffic.
-Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows, bool tree) {
   Plan plan;
   plan.tiles = rows > kRows;
   plan.step = plan.tiles ? kTileKeys : kStep;
@@ -495,7 +538,7 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   plan.steps = (int32_t)steps;
   int64_t splits = 1;
   if (!plan.tiles) {
-    splits = std::min<int64_t>(heads > 0 ? 3 * kSms / heads : 1, steps / (2 * kWarps));
+    splits = std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / heads - (tree ? 1 : 0), steps / (2 * kWarps));
   } else {
     const bool pair = rows > kTileRows;
     const int64_t base = heads * ((rows + (pair ? 2 : 1) * kTileRows - 1) / ((pair ? 2 : 1) * kTileRows));
@@ -516,7 +559,7 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   return plan;
 }
 
-template <bool kExtras>
+template <bool kExtras, int kTiles>
 cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
   static std::atomic<bool> ready[64];
   int dev = 0;
@@ -524,18 +567,18 @@ cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_relaxed)) {  // doing it twice is harmless
-    e = cudaFuncSetAttribute(attend_rows_kernel<kExtras>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    e = cudaFuncSetAttribute(attend_rows_kernel<kExtras, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_relaxed);
   }
-  return launch_pdl(attend_rows_kernel<kExtras>, grid, kThreads, sizeof(Shared), s, p);
+  return launch_pdl(attend_rows_kernel<kExtras, kTiles>, grid, kThreads, sizeof(Shared), s, p);
 }
 
 }  // namespace
 }  // namespace attend
 
 size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
-  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows);
+  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows, false);  // a tree's splits are no more
   return (size_t)(plan.splits + 1) * heads * rows * (attend::kD + 1) * sizeof(float);
 }
 
@@ -560,7 +603,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.by_group = FastDiv((uint32_t)p.group);
   p.n_slots = a.n_slots;
   p.rows = a.tq * p.group;
-  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows);
+  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows, a.parents != nullptr);
   int32_t steps = 0;
   for (int i = 0; i < a.n_slots; ++i) {
     p.slots[i] = a.slots[i];
@@ -601,8 +644,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   const dim3 grid(p.parts, p.heads);
   cudaError_t e;
   if (plan.tiles) e = launch_attend_tiles(p, s);
-  else if (p.cap > 0.0f || p.slopes || p.k_doc) e = launch_rows<true>(p, grid, s);
-  else e = launch_rows<false>(p, grid, s);
+  else if (p.cap > 0.0f || p.slopes || p.k_doc)
+    e = p.rows <= 8 ? launch_rows<true, 1>(p, grid, s) : launch_rows<true, 2>(p, grid, s);
+  else
+    e = p.rows <= 8 ? launch_rows<false, 1>(p, grid, s) : launch_rows<false, 2>(p, grid, s);
   if (e != cudaSuccess || p.parts == 1) return e;
   // few parts: a warp a row; more: eight warps share a row's
   if (p.parts <= 8) return launch_pdl(attend_join_kernel<1>, dim3((unsigned)((p.rows + 7) / 8), p.heads), 256, 0, s, p);

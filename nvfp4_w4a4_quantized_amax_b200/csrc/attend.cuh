@@ -24,7 +24,9 @@ namespace attend {
 constexpr int kD = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kShift = 14.0f;  // weights are scaled by 2^kShift
+// The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
+// rarely rescaled; a row's largest weight is then between 2^kUp and 2^(kUp + kLazy) = 2^14.
+constexpr float kLazy = 4.0f, kUp = 10.0f;
 
 struct Params {
   const uint8_t* base;
@@ -72,8 +74,8 @@ struct SlotView {
   float gk;    // g_K
   float lg;    // log2(g_V / largest g_V): p 2^lg goes to the product, p to the sum
   float inv;   // 2^-lg
-  int ok;      // the slot holds the stated number of tokens
-  int vzero;   // its values count as zero: g_V is 0 or under 2^-60 of the largest
+  int16_t ok;     // the slot holds the stated number of tokens
+  int16_t vzero;  // its values count as zero: g_V is 0 or under 2^-60 of the largest
 };
 
 // Reads the listed slots' scales, one warp; *top_out = the largest g_V, 1 where all are 0.  The
@@ -124,6 +126,12 @@ __device__ __forceinline__ int query_exponent(unsigned top) {
   return e > 120 ? 120 : e;  // 2^e and 2^-e stay FP32 numbers
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float r;

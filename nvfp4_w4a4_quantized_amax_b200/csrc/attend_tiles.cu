@@ -43,10 +43,6 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsDecode = 72, kRegsIssue = 80;
 static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsIssue == 5 * kRegsLaunch, "the register split must balance");
 
-// The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
-// rarely rescaled; a row's largest weight is then between 2^kUp and 2^(kUp + kLazy) = 2^14.
-constexpr float kLazy = 4.0f, kUp = 10.0f;
-
 struct Control {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2][2], p_ready[2][2], o_done[2], done[2];  // [tile][buffer]
@@ -136,12 +132,6 @@ __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // A listed key step: the cache row (slot * chunk_tokens + token) of its first key; its number of
 // keys (bits 0..7), list entry of its slot (8..15) and whether every row sees all of it (16).

@@ -12,6 +12,7 @@ Start / NVFP4": a dtype cast of the pipeline would corrupt the quantized buffers
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -88,6 +89,8 @@ EXPORTS = ["nvfp4_version", "nvfp4_status_string", "nvfp4_scales_bytes", "nvfp4_
 def library():
     """Load libnvfp4.so (raises ImportError when it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -174,8 +177,8 @@ def _check(status: int, where: str):
 def _stream(stream):
     import torch
 
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: building a Stream object costs several microseconds a call
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -419,20 +422,30 @@ def kv_window_context(cache: KVCache, slots: Sequence[int], tokens: Sequence[int
                                        _stream(stream)), "kv_window_context")
 
 
-def _together(**tensors):
-    """Every given tensor is on one CUDA device; returns a guard that makes it the current one."""
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _together(names: str, *tensors):
+    """Every given tensor (None: not given) is on one CUDA device; returns a guard that makes it the
+    current one."""
     import torch
 
-    dev = None
-    for name, t in tensors.items():
+    dev = -1
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, other arguments are on {dev}")
-        dev = t.device
-    return torch.cuda.device(dev)
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{names.split()[i]}: a CUDA tensor is required, got one on {t.device}")
+        if dev >= 0 and d != dev:
+            raise ValueError(f"{names.split()[i]}: on {t.device}, other arguments are on cuda:{dev}")
+        dev = d
+    return _NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _at(t):
+    """Device address of a tensor whose device has been checked (None stays NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def nvfp4_rmsnorm_quantize(x, out: NVFP4Tensor, weight=None, eps: float = 1e-6, residual=None, h_out=None,
@@ -450,12 +463,12 @@ def nvfp4_rmsnorm_quantize(x, out: NVFP4Tensor, weight=None, eps: float = 1e-6, 
         raise ValueError("weight: a contiguous [cols] tensor is required")
     _scalar(gscale_in, "gscale_in")
     _scalar(amax_out, "amax_out")
-    with _together(x=x, residual=residual, weight=weight, h_out=h_out, gscale_in=gscale_in, amax_out=amax_out,
-                   out=out.codes):
+    with _together("x residual weight h_out gscale_in amax_out out", x, residual, weight, h_out, gscale_in, amax_out,
+                   out.codes):
         _check(library().nvfp4_rmsnorm_quantize(
-            _ptr(x), _dtype_code(x), rows, cols, _pitch(x), _ptr(residual), _pitch(residual), _ptr(weight),
-            _dtype_code(weight) if weight is not None else FP32, float(eps), _ptr(h_out), _pitch(h_out),
-            _ptr(gscale_in), ctypes.byref(out.c), _ptr(amax_out), _stream(stream)), "nvfp4_rmsnorm_quantize")
+            _at(x), _dtype_code(x), rows, cols, _pitch(x), _at(residual), _pitch(residual), _at(weight),
+            _dtype_code(weight) if weight is not None else FP32, eps, _at(h_out), _pitch(h_out),
+            _at(gscale_in), ctypes.byref(out.c), _at(amax_out), _stream(stream)), "nvfp4_rmsnorm_quantize")
 
 
 def _matrix(t, name: str):
@@ -534,9 +547,9 @@ def nvfp4_rope(x, table: RopeTable, positions=0, y=None, layout: int = ROPE_HALF
         raise ValueError("y: x's type and shape are required")
     pos, pos0 = _positions(positions, n, "positions")
     ld = [t.stride(0) if n > 1 else h * d for t in (x, y)]
-    with _together(x=x, y=y, positions=pos, table=table.freq):
-        _check(library().nvfp4_rope(_ptr(x), _dtype_code(x), n, h, d, ld[0], _ptr(table.freq), table.rot_dim, layout,
-                                    table.mscale, _ptr(pos), pos0, _ptr(y), ld[1], _stream(stream)), "nvfp4_rope")
+    with _together("x y positions table", x, y, pos, table.freq):
+        _check(library().nvfp4_rope(_at(x), _dtype_code(x), n, h, d, ld[0], _at(table.freq), table.rot_dim, layout,
+                                    table.mscale, _at(pos), pos0, _at(y), ld[1], _stream(stream)), "nvfp4_rope")
 
 
 def kv_attention_workspace_bytes(cache: KVCache, tokens: Sequence[int], tq: int, q_heads: int) -> int:
@@ -578,26 +591,26 @@ def _attend(where, cache, slots, tokens, q, scale, o_out, lse_out, softcap, slop
     pos, pos0 = _positions(q_pos, tq, "q_pos")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor is required")
-    with _together(q=q, o_out=o_out, lse_out=lse_out, slopes=slopes, q_doc=q_doc, k_doc=k_doc, q_pos=pos, k_new=k_new,
-                   v_new=v_new, parents=parents, workspace=workspace, cache=cache.buffer):
+    with _together("q o_out lse_out slopes q_doc k_doc q_pos k_new v_new parents workspace cache", q, o_out, lse_out,
+                   slopes, q_doc, k_doc, pos, k_new, v_new, parents, workspace, cache.buffer):
         if workspace is None:  # on the call's stream: the allocator reuses it behind the call's work
             nbytes = kv_attention_workspace_bytes(cache, tokens, tq, heads)
             with torch.cuda.stream(stream):
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         n = len(slots)
-        sarr, tarr = (ctypes.c_int32 * n)(*slots), (ctypes.c_int32 * n)(*tokens)
+        arr = ctypes.c_int32 * n
         parr = None if slot_pos is None else (ctypes.c_int64 * n)(*slot_pos)
-        at = nvfp4_attention(float(scale), float(softcap), _ptr(slopes), 1 if causal else 0, 0, window, prefix, parr,
-                             pos0, _ptr(pos), _ptr(q_doc), _ptr(k_doc), _ptr(workspace),
-                             workspace.numel() * workspace.element_size())
-        ldq, ldo = (t.stride(0) if tq > 1 else heads * shape[2] for t in (q, o_out))
-        head = (ctypes.byref(cache.handle), sarr, tarr, n, _ptr(q), tq, heads, ldq)
-        tail = (ctypes.byref(at), _ptr(o_out), ldo, _ptr(lse_out), _stream(stream))
+        at = nvfp4_attention(scale, softcap, _at(slopes), 1 if causal else 0, 0, window, prefix, parr, pos0, _at(pos),
+                             _at(q_doc), _at(k_doc), _at(workspace), workspace.nbytes)
+        dense = heads * shape[2]
+        ldq, ldo = (q.stride(0), o_out.stride(0)) if tq > 1 else (dense, dense)
+        head = (ctypes.byref(cache.handle), arr(*slots), arr(*tokens), n, _at(q), tq, heads, ldq)
+        tail = (ctypes.byref(at), _at(o_out), ldo, _at(lse_out), _stream(stream))
         if parents is None:
             _check(library().kv_window_attention(*head, *tail), where)
         else:
             ld_new = k_new.stride(0) if tq > 1 else cache.heads * cache.head_dim
-            _check(library().kv_tree_attention(*head, _ptr(k_new), _ptr(v_new), ld_new, _ptr(parents), *tail), where)
+            _check(library().kv_tree_attention(*head, _at(k_new), _at(v_new), ld_new, _at(parents), *tail), where)
 
 
 def kv_window_attention(cache: KVCache, slots: Sequence[int], tokens: Sequence[int], q, scale: float, o_out,

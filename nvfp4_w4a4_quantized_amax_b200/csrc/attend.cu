@@ -209,6 +209,20 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
 #pragma unroll
     for (int e = 0; e < 2; ++e) m[u][e] = -INFINITY, l[u][e] = 0.0f, bias[u][e] = mul[u][e] = 0.0f;
   }
+  int qpos[kTiles][2];
+  float slope[kTiles][2];
+  const float cap = kExtras ? p.cap * kLog2e : 0.0f;
+#pragma unroll
+  for (int u = 0; u < kTiles; ++u) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (int)min((int64_t)(8 * u + 2 * c + e), p.rows - 1);
+      qpos[u][e] = positions ? sh.row_pos[8 * u + 2 * c + e] : 0;
+      slope[u][e] = 0.0f;
+      if (kExtras && p.slopes)
+        slope[u][e] = kLog2e * p.slopes[h * p.group + (r - (int)p.by_group.div((uint32_t)r) * p.group)];
+    }
+  }
   int seg_at = -1;
   float lg = 0.0f, inv = 1.0f;
   bool vzero = false;
@@ -246,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float fac = sh.row_fac[8 * u + 2 * c + e];
-          const float f = kExtras && p.cap > 0.0f ? fac : fac * kLog2e;  // log2 units without a cap
+          // log2 units, or shares of the cap
+          const float f = kExtras && p.cap > 0.0f ? fac / p.cap : fac * kLog2e;
           bias[u][e] = __shfl_sync(0xFFFFFFFFu, acc[u], 4 * (2 * c + e)) * f;
           mul[u][e] = f * sv.gk;
         }
@@ -284,34 +299,29 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
         }
       }
       const int kp0 = p.pos[seg_at] + si.t0;
+      const int32_t* docs = p.k_doc;
+      if (kExtras && docs) {
+        docs += si.t0;
+        for (int i = 0; i < seg_at; ++i) docs += p.tokens[i];
+      }
       bool grow = false;
 #pragma unroll
       for (int u = 0; u < kTiles; ++u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int e = k & 1;
-          const int rr = 8 * u + 2 * c + e;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             float x = fmaf(s[t][u][k], mul[u][e], bias[u][e]);
             if (kExtras || si.vis == 1) {
               const int key = 16 * t + 8 * (k >> 1) + tile_key(g);
-              const int qpos = positions ? sh.row_pos[rr] : 0;
               if (kExtras) {
-                if (p.cap > 0.0f) x = softcap(x, p.cap * kLog2e, 2.0f * kLog2e / p.cap);
-                if (p.slopes) {
-                  const int r = (int)min((int64_t)rr, p.rows - 1);
-                  const float slope = p.slopes[h * p.group + (r - (int)p.by_group.div((uint32_t)r) * p.group)];
-                  x = fmaf(-slope * kLog2e, fabsf((float)(qpos - (kp0 + key))), x);
-                }
+                if (p.cap > 0.0f) x = softcap(x, cap, 2.0f * kLog2e);
+                if (p.slopes) x = fmaf(-slope[u][e], fabsf((float)(qpos[u][e] - (kp0 + key))), x);
               }
               if (si.vis == 1) {
-                bool see = key < si.n && visible(p, kp0 + key, qpos);
-                if (kExtras && p.k_doc) {
-                  const int32_t* docs = p.k_doc;
-                  for (int i = 0; i < seg_at; ++i) docs += p.tokens[i];
-                  see = see && docs[si.t0 + min(key, si.n - 1)] == sh.row_doc[rr];
-                }
+                bool see = key < si.n && visible(p, kp0 + key, qpos[u][e]);
+                if (kExtras && p.k_doc) see = see && docs[min(key, si.n - 1)] == sh.row_doc[8 * u + 2 * c + e];
                 if (!see) x = -INFINITY;
               }
             }

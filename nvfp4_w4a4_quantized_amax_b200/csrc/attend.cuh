@@ -145,6 +145,22 @@ __device__ __forceinline__ float softcap(float x, float cap, float two_log2e_ove
   return cap - 2.0f * cap * rcp_approx(1.0f + ex2(x * two_log2e_over_cap));
 }
 
+// tanh z for |z| <= kTanhNear: z times a polynomial in z^2, interpolated at the Chebyshev nodes of
+// [0, kTanhNear^2] (the series' nearest singularity, z = i pi / 2, is far: five terms are within
+// 2^-23 of tanh).  Scores are mostly well inside their cap, and this runs on the FMA units, two
+// lanes at a time, where softcap takes two of the sixteen special-function results a cycle that
+// the softmax's own exponentials need.
+constexpr float kTanhNear = 0.625f;
+__device__ __forceinline__ void tanh_near2(float& a, float& b) {
+  float ua, ub, pa = 0.015043356455862522f, pb = pa;
+  mul2(ua, ub, a, b, a, b);
+  fma2(pa, pb, pa, pb, ua, ub, -0.05181591212749481f, -0.05181591212749481f);
+  fma2(pa, pb, pa, pb, ua, ub, 0.1330437958240509f, 0.1330437958240509f);
+  fma2(pa, pb, pa, pb, ua, ub, -0.33331942558288574f, -0.33331942558288574f);
+  fma2(pa, pb, pa, pb, ua, ub, 0.9999998807907104f, 0.9999998807907104f);
+  mul2(a, b, a, b, pa, pb);
+}
+
 // The visibility of keys [k0, k1] (positions) to queries [q0, q1]: 0 none, 1 some, 2 all.
 __device__ __forceinline__ int visibility(const Params& p, int k0, int k1, int q0, int q1) {
   if (p.prefix > 0 && k0 < p.prefix) {

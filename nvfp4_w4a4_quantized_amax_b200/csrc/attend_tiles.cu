@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
           f16x2_to_f32x2(v.w, x, y);
           acc0 = fmaf(x, m1.z, acc0), acc1 = fmaf(y, m1.w, acc1);
         }
-        const float f = kExtras && p.cap > 0.0f ? fac : fac * kLog2e;  // log2 units without a cap
+        // log2 units, or shares of the cap
+        const float f = kExtras && p.cap > 0.0f ? fac / p.cap : fac * kLog2e;
         bias = (acc0 + acc1) * f;
         mul = f * sv.gk;
       }
@@ -536,9 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(s[e], mul, bias);
         if (kExtras && p.cap > 0.0f) {
-          const float twice = 2.0f * kLog2e / p.cap, cap = p.cap * kLog2e;
+          const float cap = p.cap * kLog2e;
+          float far = 0.0f;
 #pragma unroll
-          for (int e = 0; e < kTileKeys; ++e) s[e] = softcap(s[e], cap, twice);
+          for (int e = 0; e < kTileKeys; e += 2) far = fmaxf(far, fmaxf(fabsf(s[e]), fabsf(s[e + 1])));
+          if (__all_sync(0xFFFFFFFFu, far <= kTanhNear)) {
+#pragma unroll
+            for (int e = 0; e < kTileKeys; e += 2) {
+              tanh_near2(s[e], s[e + 1]);
+              mul2(s[e], s[e + 1], s[e], s[e + 1], cap, cap);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kTileKeys; ++e) s[e] = softcap(s[e], cap, 2.0f * kLog2e);
+          }
         }
         if (kExtras && p.slopes) {
           const float d0 = (float)(qpos - kp0);

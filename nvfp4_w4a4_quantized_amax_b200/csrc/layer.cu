@@ -50,7 +50,7 @@ struct NormParams {
   const float* gscale_in;
   float* gscale_out;
   unsigned* amax;  // nullable with a supplied scale
-  bool amax_store; // one CTA sees every row: it stores the maximum instead of accumulating it
+  bool amax_store;  // CTA 0 sees every row: it stores the maximum instead of accumulating it
   unsigned* status;
 };
 
@@ -183,8 +183,11 @@ __device__ __forceinline__ double row_sum(double v, double* red, int warps) {
   return s;
 }
 
+// Three CTAs of 256 threads an SM (85 registers; two for FP32, whose rows take twice as many): the rows' reads, reduction and encoding follow one
+// another within a CTA, so others have to fill in (8192 x 9216 with residual: two CTAs 122 us, three
+// 107, four 117, five 135).
 template <bool kBf16, bool kMma, int kMode, int kLanes>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParams p) {
   __shared__ double red[kThreads / 32];
   __shared__ unsigned redm[kThreads / 32];
   pdl_trigger();
@@ -214,8 +217,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormParams p) {
   unsigned local_max = 0;
   // every thread of the CTA takes the same number of steps: the reductions are collective
   for (int64_t base = (int64_t)blockIdx.x * per_cta; base < row_end; base += (int64_t)gridDim.x * per_cta) {
-    const int64_t row = base + threadIdx.x / lanes;
-    const bool live = row < p.rows;
+    // the second pass goes backwards: the first one's latest rows are the most likely still in L2
+    const int64_t at = base + threadIdx.x / lanes, row = kMode == kEncode ? row_end - 1 - at : at;
+    const bool live = row >= 0 && row < p.rows;
     Block<kBf16> kept[kCached];
     double ss = 0.0;
     if (live) {
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormParams p) {
         if (encodes) norm_encode<kMma>(p, row, j, y, m, g, d6, r6);
       }
     }
-    if (kMma && encodes && row < p.vrows)  // padding of the tensor-core scale layout
+    if (kMma && encodes && row >= 0 && row < p.vrows)  // padding of the tensor-core scale layout
       for (int32_t j = live ? p.nb + lane : lane; j < p.vnb; j += lanes) p.scales[sf_mma_offset(row, j, p.groups)] = 0;
   }
   if (kMode == kEncode) return;
@@ -271,14 +275,19 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormParams p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < warps; ++w) local_max = max(local_max, redm[w]);
-    if (p.amax_store) *p.amax = local_max;
+    if (p.amax_store && blockIdx.x == 0) *p.amax = local_max;
     else if (local_max != 0u) atomicMax(p.amax, local_max);
   }
 }
 
 template <bool kBf16, bool kMma, int kMode, int kLanes>
-cudaError_t launch_norm_kernel(const NormParams& p, int threads, cudaStream_t s) {
+cudaError_t launch_norm_kernel(NormParams p, int threads, cudaStream_t s) {
   const int per_cta = kLanes > 32 ? 1 : threads / kLanes;
+  p.amax_store = p.rows <= per_cta;
+  if (kMode != kEncode && p.amax && !p.amax_store) {
+    const cudaError_t e = launch_zero_words(p.amax, 1, s);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t rows = kMma && kMode != kAmax ? p.vrows : p.rows;
   // one wave of CTAs; a row a CTA (or 8 or 32 of them) at a time
   static std::atomic<int> resident[64][kThreads / 32 + 1];  // per device and CTA size; racing writers agree
@@ -311,17 +320,9 @@ cudaError_t launch_norm_mode(const NormParams& p, cudaStream_t s) {
 }
 
 template <bool kBf16, bool kMma>
-cudaError_t launch_norm(NormParams& p, cudaStream_t s) {
-  if (p.gscale_in) {
-    if (p.amax) {
-      cudaError_t e = launch_zero_words(p.amax, 1, s);
-      if (e != cudaSuccess) return e;
-    }
-    return launch_norm_mode<kBf16, kMma, kGiven>(p, s);
-  }
-  cudaError_t e = launch_zero_words(p.amax, 1, s);
-  if (e != cudaSuccess) return e;
-  e = launch_norm_mode<kBf16, kMma, kAmax>(p, s);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  if (p.gscale_in) return launch_norm_mode<kBf16, kMma, kGiven>(p, s);
+  const cudaError_t e = launch_norm_mode<kBf16, kMma, kAmax>(p, s);
   if (e != cudaSuccess) return e;
   return launch_norm_mode<kBf16, kMma, kEncode>(p, s);
 }
@@ -357,6 +358,8 @@ template <bool kBf16, bool kInterleaved, bool kVector>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
   constexpr int kEsz = kBf16 ? 2 : 4;
   constexpr int kVec = kVector ? 16 / kEsz : 1;          // elements of one 16-byte access
+  // items a thread reads at a time: 64 bytes on their way where an item is one 16-byte read
+  constexpr int kRopeBatch = kInterleaved ? 4 : 2;
   constexpr int kPairs = kVector ? (kInterleaved ? kVec / 2 : kVec) : 1;  // pairs an item
   extern __shared__ float2 trig[];  // [token][pair group of 2][item] (two pairs = one 16-byte read)
   pdl_trigger();
@@ -378,86 +381,103 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
   }
   __syncthreads();
   const int n = nt * nh * p.units;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint32_t q = p.by_units.div((uint32_t)i);
-    const int u = i - (int)q * p.units;
-    const uint32_t t = nh == p.head_split ? p.by_heads.div(q) : p.by_last_heads.div(q);
-    const int h = h0 + (int)q - (int)t * nh;
-    const uint8_t* src = p.x + (t0 + t) * p.x_pitch + (int64_t)h * p.head_bytes;
-    uint8_t* dst = p.y + (t0 + t) * p.y_pitch + (int64_t)h * p.head_bytes;
-    if (u >= p.turned) {  // elements behind the rotated ones
-      const int64_t off = (int64_t)2 * p.half * kEsz + (int64_t)(u - p.turned) * kVec * kEsz;
-      if (kVector) stg_v4(dst + off, ldg_v4(src + off));
-      else if (kBf16) *reinterpret_cast<uint16_t*>(dst + off) = *reinterpret_cast<const uint16_t*>(src + off);
-      else *reinterpret_cast<uint32_t*>(dst + off) = *reinterpret_cast<const uint32_t*>(src + off);
-      continue;
-    }
-    float a[kPairs], b[kPairs];
-    const int64_t oa = (int64_t)u * kPairs * (kInterleaved ? 2 : 1) * kEsz;
-    const int64_t ob = kInterleaved ? oa + kEsz : oa + (int64_t)p.half * kEsz;
-    if (kVector) {
-      const uint4 va = ldg_v4(src + oa);
-      const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
-      if (kInterleaved) {
+  for (int i0 = threadIdx.x; i0 < n; i0 += kRopeBatch * kThreads) {
+    // kRopeBatch items' reads on their way before the first is used
+    const uint8_t* src[kRopeBatch];
+    uint8_t* dst[kRopeBatch];
+    int item[kRopeBatch], token[kRopeBatch];
+    int64_t oa[kRopeBatch], ob[kRopeBatch];
+    uint4 va[kRopeBatch], vb[kRopeBatch];
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-          a[k] = kBf16 ? bf16_lo(wa[k]) : __uint_as_float(wa[(2 * k) & 3]);
-          b[k] = kBf16 ? bf16_hi(wa[k]) : __uint_as_float(wa[(2 * k + 1) & 3]);
-        }
-      } else {
-        const uint4 vb = ldg_v4(src + ob);
-        const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-          a[k] = !kBf16 ? __uint_as_float(wa[k & 3]) : (k & 1) ? bf16_hi(wa[k / 2]) : bf16_lo(wa[k / 2]);
-          b[k] = !kBf16 ? __uint_as_float(wb[k & 3]) : (k & 1) ? bf16_hi(wb[k / 2]) : bf16_lo(wb[k / 2]);
-        }
-      }
-    } else if (kBf16) {
-      a[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + oa) << 16);
-      b[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + ob) << 16);
-    } else {
-      a[0] = *reinterpret_cast<const float*>(src + oa);
-      b[0] = *reinterpret_cast<const float*>(src + ob);
-    }
-    float oa_v[kPairs], ob_v[kPairs];
-#pragma unroll
-    for (int k = 0; k < kPairs; k += 2) {
-      float2 cs[2];
+    for (int x = 0; x < kRopeBatch; ++x) {
+      const int i = i0 + x * kThreads;
+      if (i >= n) break;
+      const uint32_t q = p.by_units.div((uint32_t)i);
+      item[x] = i - (int)q * p.units;
+      token[x] = (int)(nh == p.head_split ? p.by_heads.div(q) : p.by_last_heads.div(q));
+      const int h = h0 + (int)q - token[x] * nh;
+      src[x] = p.x + (t0 + token[x]) * p.x_pitch + (int64_t)h * p.head_bytes;
+      dst[x] = p.y + (t0 + token[x]) * p.y_pitch + (int64_t)h * p.head_bytes;
+      // a rotated item's a (and b); one behind them copies what follows the rotated elements
+      const bool turned = item[x] < p.turned;
+      oa[x] = turned ? (int64_t)item[x] * kPairs * (kInterleaved ? 2 : 1) * kEsz
+                     : (int64_t)2 * p.half * kEsz + (int64_t)(item[x] - p.turned) * kVec * kEsz;
+      ob[x] = kInterleaved ? oa[x] + kEsz : oa[x] + (int64_t)p.half * kEsz;
       if (kVector) {
-        const float4 v = *reinterpret_cast<const float4*>(&trig[(int)t * p.half + (k / 2) * (2 * p.turned) + u * 2]);
-        cs[0] = make_float2(v.x, v.y);
-        cs[1] = make_float2(v.z, v.w);
+        va[x] = ldg_v4(src[x] + oa[x]);
+        if (!kInterleaved && turned) vb[x] = ldg_v4(src[x] + ob[x]);
+      } else if (kBf16) {
+        va[x].x = (uint32_t)*reinterpret_cast<const uint16_t*>(src[x] + oa[x]) << 16;
+        if (turned) vb[x].x = (uint32_t)*reinterpret_cast<const uint16_t*>(src[x] + ob[x]) << 16;
       } else {
-        cs[0] = trig[(int)t * p.half + u];
-      }
-#pragma unroll
-      for (int e = 0; e < 2 && k + e < kPairs; ++e) {
-        oa_v[k + e] = fmaf(a[k + e], cs[e].x, -(b[k + e] * cs[e].y));
-        ob_v[k + e] = fmaf(a[k + e], cs[e].y, b[k + e] * cs[e].x);
+        va[x].x = *reinterpret_cast<const uint32_t*>(src[x] + oa[x]);
+        if (turned) vb[x].x = *reinterpret_cast<const uint32_t*>(src[x] + ob[x]);
       }
     }
-    if (kVector) {
-      uint32_t wa[4], wb[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (kInterleaved) {
-          wa[k] = kBf16 ? pack_bf16x2(oa_v[k % kPairs], ob_v[k % kPairs])
-                        : __float_as_uint((k & 1) ? ob_v[(k / 2) % kPairs] : oa_v[(k / 2) % kPairs]);
+    for (int x = 0; x < kRopeBatch; ++x) {
+      if (i0 + x * kThreads >= n) break;
+      if (item[x] >= p.turned) {
+        if (kVector) stg_v4(dst[x] + oa[x], va[x]);
+        else if (kBf16) *reinterpret_cast<uint16_t*>(dst[x] + oa[x]) = (uint16_t)(va[x].x >> 16);
+        else *reinterpret_cast<uint32_t*>(dst[x] + oa[x]) = va[x].x;
+        continue;
+      }
+      float a[kPairs], b[kPairs];
+      const uint32_t wa[4] = {va[x].x, va[x].y, va[x].z, va[x].w}, wb[4] = {vb[x].x, vb[x].y, vb[x].z, vb[x].w};
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) {
+        if (!kVector) {
+          a[k] = __uint_as_float(wa[0]);
+          b[k] = __uint_as_float(wb[0]);
+        } else if (kInterleaved) {
+          a[k] = kBf16 ? bf16_lo(wa[k & 3]) : __uint_as_float(wa[(2 * k) & 3]);
+          b[k] = kBf16 ? bf16_hi(wa[k & 3]) : __uint_as_float(wa[(2 * k + 1) & 3]);
         } else {
-          wa[k] = kBf16 ? pack_bf16x2(oa_v[(2 * k) % kPairs], oa_v[(2 * k + 1) % kPairs]) : __float_as_uint(oa_v[k % kPairs]);
-          wb[k] = kBf16 ? pack_bf16x2(ob_v[(2 * k) % kPairs], ob_v[(2 * k + 1) % kPairs]) : __float_as_uint(ob_v[k % kPairs]);
+          a[k] = !kBf16 ? __uint_as_float(wa[k & 3]) : (k & 1) ? bf16_hi(wa[(k / 2) & 3]) : bf16_lo(wa[(k / 2) & 3]);
+          b[k] = !kBf16 ? __uint_as_float(wb[k & 3]) : (k & 1) ? bf16_hi(wb[(k / 2) & 3]) : bf16_lo(wb[(k / 2) & 3]);
         }
       }
-      stg_v4(dst + oa, make_uint4(wa[0], wa[1], wa[2], wa[3]));
-      if (!kInterleaved) stg_v4(dst + ob, make_uint4(wb[0], wb[1], wb[2], wb[3]));
-    } else if (kBf16) {
-      const uint32_t v = pack_bf16x2(oa_v[0], ob_v[0]);
-      *reinterpret_cast<uint16_t*>(dst + oa) = (uint16_t)(v & 0xFFFFu);
-      *reinterpret_cast<uint16_t*>(dst + ob) = (uint16_t)(v >> 16);
-    } else {
-      *reinterpret_cast<float*>(dst + oa) = oa_v[0];
-      *reinterpret_cast<float*>(dst + ob) = ob_v[0];
+      float ra[kPairs], rb[kPairs];
+#pragma unroll
+      for (int k = 0; k < kPairs; k += 2) {
+        float2 cs[2];
+        if (kVector) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(&trig[token[x] * p.half + (k / 2) * (2 * p.turned) + item[x] * 2]);
+          cs[0] = make_float2(v.x, v.y);
+          cs[1] = make_float2(v.z, v.w);
+        } else {
+          cs[0] = trig[token[x] * p.half + item[x]];
+        }
+#pragma unroll
+        for (int e = 0; e < 2 && k + e < kPairs; ++e) {
+          ra[k + e] = fmaf(a[k + e], cs[e].x, -(b[k + e] * cs[e].y));
+          rb[k + e] = fmaf(a[k + e], cs[e].y, b[k + e] * cs[e].x);
+        }
+      }
+      if (kVector) {
+        uint32_t sa[4], sb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (kInterleaved) {
+            sa[k] = kBf16 ? pack_bf16x2(ra[k % kPairs], rb[k % kPairs])
+                          : __float_as_uint((k & 1) ? rb[(k / 2) % kPairs] : ra[(k / 2) % kPairs]);
+          } else {
+            sa[k] = kBf16 ? pack_bf16x2(ra[(2 * k) % kPairs], ra[(2 * k + 1) % kPairs]) : __float_as_uint(ra[k % kPairs]);
+            sb[k] = kBf16 ? pack_bf16x2(rb[(2 * k) % kPairs], rb[(2 * k + 1) % kPairs]) : __float_as_uint(rb[k % kPairs]);
+          }
+        }
+        stg_v4(dst[x] + oa[x], make_uint4(sa[0], sa[1], sa[2], sa[3]));
+        if (!kInterleaved) stg_v4(dst[x] + ob[x], make_uint4(sb[0], sb[1], sb[2], sb[3]));
+      } else if (kBf16) {
+        const uint32_t v = pack_bf16x2(ra[0], rb[0]);
+        *reinterpret_cast<uint16_t*>(dst[x] + oa[x]) = (uint16_t)(v & 0xFFFFu);
+        *reinterpret_cast<uint16_t*>(dst[x] + ob[x]) = (uint16_t)(v >> 16);
+      } else {
+        *reinterpret_cast<float*>(dst[x] + oa[x]) = ra[0];
+        *reinterpret_cast<float*>(dst[x] + ob[x]) = rb[0];
+      }
     }
   }
 }

@@ -40,7 +40,7 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // Registers: the launch's 96 a thread (20 warps, five on each of the SM's four files) are moved
 // between the warpgroups.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsDecode = 72, kRegsIssue = 80;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsDecode = 64, kRegsIssue = 80;
 static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsIssue == 5 * kRegsLaunch, "the register split must balance");
 
 struct Control {
@@ -51,7 +51,7 @@ struct Control {
   int32_t listed;
   int32_t q_first, q_last;
   float gv_top;
-  int32_t row_doc[256];
+  int32_t row_pos[256], row_doc[256];
   float row_fac[256];  // factor of a row's products: scale and the power of two of its queries
   SlotView view[kMaxWindowSlots];
   float m[128], l[128];  // of tile 1, when the two are joined
@@ -190,26 +190,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   __syncthreads();
-  // this thread's row (threads 0..255; the last row for those behind the end): position, document
-  const int tile = (warp >> 2) & 1;
-  const int64_t row = r0 + (kPair ? tile * 128 : 0) + (threadIdx.x & 127);
-  const bool live = warp < 8 && row < r_end;
-  int qpos = 0, qdoc = 0;
-  float slope = 0.0f;
-  if (warp < 8) {
-    const int64_t rr = row < r_end ? row : r_end - 1;
-    const int64_t i = p.by_group.div((uint32_t)rr);
-    if (positions) qpos = row_position(p, parents, rr);
-    if (kExtras && p.q_doc) qdoc = p.q_doc[i];
-    if (kExtras && p.slopes) slope = p.slopes[h * p.group + (int)(rr - i * p.group)] * kLog2e;
-    if (kPair || tile == 0) {
-      const int lo = __reduce_min_sync(0xFFFFFFFFu, qpos), hi = __reduce_max_sync(0xFFFFFFFFu, qpos);
-      if (lane == 0) {
-        atomicMin(&ct.q_first, lo);
-        atomicMax(&ct.q_last, hi);
-      }
-      if (kExtras) ct.row_doc[threadIdx.x] = qdoc;
+  // the rows' positions and documents (the last row's for those behind the end), a thread a row
+  if (warp < (kPair ? 8 : 4)) {
+    const int64_t rr = r0 + threadIdx.x < r_end ? r0 + threadIdx.x : r_end - 1;
+    const int qpos = positions ? row_position(p, parents, rr) : 0;
+    const int lo = __reduce_min_sync(0xFFFFFFFFu, qpos), hi = __reduce_max_sync(0xFFFFFFFFu, qpos);
+    if (lane == 0) {
+      atomicMin(&ct.q_first, lo);
+      atomicMax(&ct.q_last, hi);
     }
+    ct.row_pos[threadIdx.x] = qpos;
+    if (kExtras) ct.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[p.by_group.div((uint32_t)rr)] : 0;
   }
   // the slots' scales by one warp, the queries by the others: half a warp a row, to binary16 scaled
   // by a power of two, into the swizzled operand tiles (zeros behind the last row)
@@ -251,9 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     fence_proxy_async_smem();
   }
   __syncthreads();
-  const float gv_top = ct.gv_top;
-  const float fac = ct.row_fac[(kPair ? tile * 128 : 0) + (threadIdx.x & 127)];
-
   // the key steps of this CTA's range that some row sees, in order
   const int first = (int)((int64_t)p.steps * part / p.splits), last = (int)((int64_t)p.steps * (part + 1) / p.splits);
   const int n_range = last - first;  // at most kMaxListed
@@ -459,6 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
   } else {
     // ------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int tile = warp >> 2, slot_row = (kPair ? tile * 128 : 0) + (threadIdx.x & 127);
+    const int64_t row = r0 + slot_row;
+    const bool live = row < r_end;
+    const int qpos = ct.row_pos[slot_row], qdoc = kExtras ? ct.row_doc[slot_row] : 0;
+    const float fac = ct.row_fac[slot_row];
+    float slope = 0.0f;
+    if (kExtras && p.slopes) {
+      const int64_t rr = live ? row : r_end - 1;
+      slope = p.slopes[h * p.group + (int)(rr - (int64_t)p.by_group.div((uint32_t)rr) * p.group)] * kLog2e;
+    }
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * 128;
     const uint8_t* qrow = qbuf + (kPair ? tile : 0) * kQBytes + (threadIdx.x & 127) * 128;
@@ -695,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         }
       }
       if (kPair || tile == 0) {
-        const float f = l == 0.0f ? 0.0f : 1.0f / l * gv_top;
+        const float f = l == 0.0f ? 0.0f : 1.0f / l * ct.gv_top;
         mine *= f;
         other *= f;
         const float log2l = l == 0.0f ? -INFINITY : m + log2f(l) - kUp;

@@ -106,11 +106,13 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
     __syncthreads();
   }
   if (tree_part) {
+    // a warp's rows, lane by lane, are those that it stores at the end: with one part it is this
+    // CTA that joins them, and each thread reads back what it wrote itself
     tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, warp, kRows, kWarps);
-    return;
+    if (p.parts > 1) return;
   }
   int q_first = 0, q_last = 0;
-  if (positions || (kExtras && p.q_doc)) {
+  if (positions || p.parents || (kExtras && p.q_doc)) {
     if (threadIdx.x < kRows) {
       const int r = (int)min((int64_t)threadIdx.x, p.rows - 1);
       sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
@@ -535,11 +537,12 @@ struct Plan {
   int32_t splits;       // CTAs that share a window
 };
 
-// Up to 16 rows a cache head: CTAs of 8 or 16 rows, as many as run at once (a tree's own part among
-// them), each with two steps a warp at least.
-// More: tiles of 128 rows; the keys are split where rows and heads do not fill the SMs evenly, by
-// the least of waves * (steps a CTA + a CTA's own cost), with the partial results' traffic.
-Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows, bool tree) {
+// Up to 16 rows a cache head take CTAs of few rows, more take tiles of 128 rows.  Either way a
+// window is split over CTAs where that pays: the least of a model of the time, with constants
+// measured on B200 (us): a step of 32 keys takes a warp 1.8 alone and 0.12 more for each warp on its
+// SM; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, and a CTA 9 besides; joining
+// costs a second launch, 5, and the partial results' traffic.
+Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   Plan plan;
   plan.tiles = rows > kRows;
   plan.step = plan.tiles ? kTileKeys : kStep;
@@ -547,25 +550,31 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows, bool
   for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + plan.step - 1) / plan.step;
   plan.steps = (int32_t)steps;
   int64_t splits = 1;
+  double best = 0.0;
+  auto consider = [&](int64_t n, double us) {
+    if (n > 1) us += 5.0 + 2.0 * n * heads * rows * 516 / 5e6;
+    if (best == 0.0 || us < best) {
+      best = us;
+      splits = n;
+    }
+  };
   if (!plan.tiles) {
-    splits = std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / heads - (tree ? 1 : 0), steps / (2 * kWarps));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / heads, steps / kWarps));
+    for (int64_t n = 1; n <= most; ++n) {
+      const int64_t mine = (steps + n * kWarps - 1) / (n * kWarps);
+      consider(n, mine * (1.8 + 0.12 * kWarps * n * heads / kSms));
+    }
   } else {
     const bool pair = rows > kTileRows;
     const int64_t base = heads * ((rows + (pair ? 2 : 1) * kTileRows - 1) / ((pair ? 2 : 1) * kTileRows));
-    const double step_us = pair ? 0.8 : 0.4, cta_us = 6.0;
-    double best = 0.0;
-    const int64_t least = (steps + kMaxListed - 1) / kMaxListed;
-    for (int64_t n = std::max<int64_t>(least, 1); n <= std::max<int64_t>(least, std::min<int64_t>(steps / 8, kSms)); ++n) {
+    const int64_t least = std::max<int64_t>((steps + kMaxListed - 1) / kMaxListed, 1);
+    const int64_t most = std::max<int64_t>(least, std::min<int64_t>(steps / 4, kSms));
+    for (int64_t n = least; n <= most; ++n) {
       const int64_t waves = (base * n + kSms - 1) / kSms;
-      const double join_us = n > 1 ? 4.0 + 2.0 * n * heads * rows * 516 / 5e6 : 0.0;
-      const double us = waves * ((steps + n - 1) / n * step_us + cta_us) + join_us;
-      if (best == 0.0 || us < best) {
-        best = us;
-        splits = n;
-      }
+      consider(n, waves * ((steps + n - 1) / n * (pair ? 1.2 : 0.65) + 9.0));
     }
   }
-  plan.splits = (int32_t)std::max<int64_t>(splits, 1);
+  plan.splits = (int32_t)splits;
   return plan;
 }
 
@@ -588,7 +597,7 @@ cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
 }  // namespace attend
 
 size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
-  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows, false);  // a tree's splits are no more
+  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows);
   return (size_t)(plan.splits + 1) * heads * rows * (attend::kD + 1) * sizeof(float);
 }
 
@@ -613,7 +622,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.by_group = FastDiv((uint32_t)p.group);
   p.n_slots = a.n_slots;
   p.rows = a.tq * p.group;
-  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows, a.parents != nullptr);
+  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows);
   int32_t steps = 0;
   for (int i = 0; i < a.n_slots; ++i) {
     p.slots[i] = a.slots[i];
@@ -646,8 +655,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.lse = a.lse;
   p.tq = a.tq;
   p.status = a.status;
-  p.parts = plan.splits + (a.parents ? 1 : 0);
-  if (p.parts > 1) {
+  p.parts = plan.splits + (a.parents && plan.splits > 1 ? 1 : 0);
+  if (p.parts > 1 || a.parents) {
     p.part_o = a.workspace;
     p.part_l = a.workspace + (int64_t)p.parts * p.heads * p.rows * kD;
   }

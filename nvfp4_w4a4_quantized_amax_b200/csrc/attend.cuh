@@ -62,7 +62,8 @@ struct Params {
   float* lse;         // [heads * group][tq], nullable
   int64_t tq;
   // partial results of `parts` sets of keys: O (normalised) [part][cache head][row][128] and
-  // log2 of the sum [part][cache head][row]
+  // log2 of the sum [part][cache head][row].  The drafts are the last part; where one CTA has the
+  // whole window there is one part, theirs, and that CTA joins it
   int32_t parts;
   float* part_o;
   float* part_l;
@@ -195,15 +196,32 @@ __device__ __forceinline__ int parent_of(const Params& p, const int32_t* parents
   return j;
 }
 
-// Where row r of cache head h keeps its result: the output itself, or a partial.  Four dims from
-// d on; log2l = log2 of the row's sum of weights.
+// Four dims from d on of row r's result among `part`, normalised; log2l: log2 of its sum of weights.
+__device__ __forceinline__ void store_partial(const Params& p, int part, int h, int64_t r, int d, float4 o,
+                                              float log2l, bool with_l) {
+  const int64_t at = ((int64_t)part * p.heads + h) * p.rows + r;
+  *reinterpret_cast<float4*>(p.part_o + at * kD + d) = o;
+  if (with_l) p.part_l[at] = log2l;
+}
+
+// A window's result of row r: a partial where several CTAs share the window, else the output, with
+// what the drafts gave (written by this CTA as the first partial) joined in.
 __device__ __forceinline__ void store_row(const Params& p, int part, int h, int64_t r, int d, float4 o, float log2l,
                                           bool with_l) {
-  if (p.parts > 1) {
-    const int64_t at = ((int64_t)part * p.heads + h) * p.rows + r;
-    *reinterpret_cast<float4*>(p.part_o + at * kD + d) = o;
-    if (with_l) p.part_l[at] = log2l;
-    return;
+  if (p.parts > 1) return store_partial(p, part, h, r, d, o, log2l, with_l);
+  if (p.parents) {
+    const int64_t at = (int64_t)h * p.rows + r;
+    const float lt = *(volatile float*)(p.part_l + at);
+    const float4 t = *reinterpret_cast<const float4*>(p.part_o + at * kD + d);
+    const float top = lt == -INFINITY && log2l == -INFINITY ? 0.0f : fmaxf(lt, log2l);
+    const float a = ex2(log2l - top), b = ex2(lt - top), inv = 1.0f / (a + b);
+    if (a + b != 0.0f) {  // a NaN of either goes on
+      o.x = (a * o.x + b * t.x) * inv;
+      o.y = (a * o.y + b * t.y) * inv;
+      o.z = (a * o.z + b * t.z) * inv;
+      o.w = (a * o.w + b * t.w) * inv;
+      log2l = top + log2f(a + b);
+    }
   }
   const int64_t i = p.by_group.div((uint32_t)r);
   const int head = h * p.group + (int)(r - i * p.group);
@@ -282,8 +300,8 @@ __device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parent
       m = top;
     }
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    store_row(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
-              l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
+    store_partial(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
+                  l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
     __syncwarp();
   }
 }

@@ -384,6 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     if (p.parents && t >= 2) {
       int16_t* ancestors = reinterpret_cast<int16_t*>(parents + kMaxTreeDrafts) + (t - 2) * kMaxTreeDrafts;
       tree_rows(p, parents, ancestors, h, r0 + 2 * part + (t - 2), r_end, 2 * p.splits);
+      if (p.parts == 1) {  // the softmax warps of this CTA join them
+        __threadfence_block();
+        asm volatile("bar.arrive 2, 320;" ::: "memory");
+      }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
@@ -658,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     }
     fence_after();
     {  // after a wait that gave up as well: every softmax warp meets at the barrier below
+      if (p.parents && p.parts == 1) asm volatile("bar.sync 2, 320;" ::: "memory");
       float other = 0.0f;  // factor of tile 1's output, when the two are joined
       float mine = 1.0f;
       if (!kPair) {

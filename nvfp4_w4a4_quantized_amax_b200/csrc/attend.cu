@@ -51,7 +51,7 @@ struct Shared {
     } join;
     struct {
       int32_t parents[kMaxTreeDrafts];
-      int16_t list[kWarps][kMaxTreeDrafts];
+      int16_t list[kWarps][kMaxFoldedDrafts];
     } tree;
   };
   StepInfo info[kWarps][kRing];
@@ -99,18 +99,14 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int part = blockIdx.x, h = blockIdx.y;
-  const bool tree_part = p.parents && part == p.parts - 1;
   const bool positions = p.causal || p.window || p.prefix || p.slopes;
-  if (p.parents && (tree_part || positions)) {
+  if (p.parents && (p.fold || positions)) {
     for (int i = threadIdx.x; i < p.drafts; i += kThreads) sh.tree.parents[i] = p.parents[i];
     __syncthreads();
   }
-  if (tree_part) {
-    // a warp's rows, lane by lane, are those that it stores at the end: with one part it is this
-    // CTA that joins them, and each thread reads back what it wrote itself
-    tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, warp, kRows, kWarps);
-    if (p.parts > 1) return;
-  }
+  // a warp's rows, lane by lane, are those that it stores at the end: each thread then reads back
+  // what it wrote itself
+  if (p.fold) tree_rows(p, sh.tree.parents, sh.tree.list[warp], h, warp, kRows, kWarps);
   int q_first = 0, q_last = 0;
   if (positions || p.parents || (kExtras && p.q_doc)) {
     if (threadIdx.x < kRows) {
@@ -527,6 +523,77 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   if (lane == 0 && p.lse) p.lse[(int64_t)head * p.tq + i] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
+// The same with a tree's drafts: kShare warps of a CTA of eight take a row, and deal out the drafts
+// that it sees and the window's parts.
+template <int kShare>
+__global__ void __launch_bounds__(256) attend_join_tree_kernel(const __grid_constant__ Params p) {
+  constexpr int kWide = 8, kJoin = 4, kAtOnce = kWide / kShare;
+  __shared__ int32_t parents[kMaxTreeDrafts];
+  __shared__ int16_t lists[kAtOnce][kMaxTreeDrafts];
+  __shared__ float part[kShare > 1 ? kWide : 1][kD], part_m[kWide], part_l[kWide];
+  __shared__ int listed[kAtOnce];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, turn = w % kShare;
+  const int h = blockIdx.y;
+  const int64_t n = (int64_t)p.heads * p.rows;
+  const int64_t r = (int64_t)blockIdx.x * kAtOnce + w / kShare;
+  const bool live = r < p.rows;
+  const int64_t rr = h * p.rows + (live ? r : 0);
+  const int i = (int)p.by_group.div((uint32_t)(live ? r : 0));
+  const int head = h * p.group + (int)((live ? r : 0) - (int64_t)i * p.group);
+  for (int j = threadIdx.x; j < p.drafts; j += 256) parents[j] = p.parents[j];
+  __syncthreads();
+  int16_t* list = lists[w / kShare];
+  if (turn == 0 && lane == 0) listed[w / kShare] = live ? ancestors_of(p, parents, i, list) : 0;
+  if (kShare > 1) __syncthreads();
+  else __syncwarp();
+  {
+    RowSum row;
+    if (live) {
+      tree_row(p, list, listed[w / kShare], turn, kShare, i, h, head, row);
+      for (int i0 = turn; i0 < p.parts; i0 += kShare * kJoin) {
+        float l[kJoin], top = -INFINITY;
+        float4 v[kJoin];
+#pragma unroll
+        for (int e = 0; e < kJoin; ++e) {
+          const int at = i0 + e * kShare < p.parts ? i0 + e * kShare : i0;
+          l[e] = p.part_l[at * n + rr];
+          v[e] = *reinterpret_cast<const float4*>(p.part_o + (at * n + rr) * kD + 4 * lane);
+          if (i0 + e * kShare >= p.parts) l[e] = -INFINITY;
+          top = l[e] != l[e] || top != top ? NAN : fmaxf(top, l[e]);
+        }
+        if (top == -INFINITY) continue;
+        row.raise(top);
+#pragma unroll
+        for (int e = 0; e < kJoin; ++e)
+          if (l[e] != -INFINITY) row.add(ex2(l[e] - row.m), v[e]);
+      }
+    }
+    if (kShare > 1) {
+      *reinterpret_cast<float4*>(&part[w][4 * lane]) = make_float4(row.o[0], row.o[1], row.o[2], row.o[3]);
+      if (lane == 0) part_m[w] = row.m, part_l[w] = row.l;
+      __syncthreads();
+    }
+    if (live && turn == 0) {
+      RowSum all = row;
+      for (int e = w + 1; e < w + kShare; ++e) {
+        if (part_m[e] == -INFINITY) continue;
+        all.raise(part_m[e]);
+        const float f = ex2(part_m[e] - all.m);
+        all.l = fmaf(f, part_l[e], all.l);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) all.o[d] = fmaf(f, part[e][4 * lane + d], all.o[d]);
+      }
+      const float inv = all.l == 0.0f ? 0.0f : 1.0f / all.l;
+      stg_v2(p.o + (int64_t)i * p.o_pitch + ((int64_t)head * kD + 4 * lane) * 2,
+             make_uint2(pack_bf16x2(all.o[0] * inv, all.o[1] * inv), pack_bf16x2(all.o[2] * inv, all.o[3] * inv)));
+      if (lane == 0 && p.lse)
+        p.lse[(int64_t)head * p.tq + i] = all.l == 0.0f ? -INFINITY : (all.m + log2f(all.l)) * kLn2;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------- host
 
 constexpr int kSms = 148;
@@ -598,7 +665,7 @@ cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
 
 size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows);
-  return (size_t)(plan.splits + 1) * heads * rows * (attend::kD + 1) * sizeof(float);
+  return (size_t)plan.splits * heads * rows * (attend::kD + 1) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
@@ -655,7 +722,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.lse = a.lse;
   p.tq = a.tq;
   p.status = a.status;
-  p.parts = plan.splits + (a.parents && plan.splits > 1 ? 1 : 0);
+  p.parts = plan.splits;
+  p.fold = a.parents && plan.splits == 1 && p.drafts <= kMaxFoldedDrafts && p.rows <= 8;
   if (p.parts > 1 || a.parents) {
     p.part_o = a.workspace;
     p.part_l = a.workspace + (int64_t)p.parts * p.heads * p.rows * kD;
@@ -667,7 +735,13 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     e = p.rows <= 8 ? launch_rows<true, 1>(p, grid, s) : launch_rows<true, 2>(p, grid, s);
   else
     e = p.rows <= 8 ? launch_rows<false, 1>(p, grid, s) : launch_rows<false, 2>(p, grid, s);
-  if (e != cudaSuccess || p.parts == 1) return e;
+  if (e != cudaSuccess) return e;
+  if (p.parents && !p.fold) {  // many drafts may be a long chain: two warps a row
+    if (p.drafts <= 64)
+      return launch_pdl(attend_join_tree_kernel<1>, dim3((unsigned)((p.rows + 7) / 8), p.heads), 256, 0, s, p);
+    return launch_pdl(attend_join_tree_kernel<2>, dim3((unsigned)((p.rows + 3) / 4), p.heads), 256, 0, s, p);
+  }
+  if (p.parts == 1) return e;
   // few parts: a warp a row; more: eight warps share a row's
   if (p.parts <= 8) return launch_pdl(attend_join_kernel<1>, dim3((unsigned)((p.rows + 7) / 8), p.heads), 256, 0, s, p);
   return launch_pdl(attend_join_kernel<8>, dim3((unsigned)p.rows, p.heads), 256, 0, s, p);

@@ -22,6 +22,7 @@ namespace nvfp4 {
 namespace attend {
 
 constexpr int kD = 128;
+constexpr int kMaxFoldedDrafts = 4;  // more are taken as the parts are joined
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum follows the true one only when that grew by more than 2^kLazy, so O is
@@ -62,9 +63,11 @@ struct Params {
   float* lse;         // [heads * group][tq], nullable
   int64_t tq;
   // partial results of `parts` sets of keys: O (normalised) [part][cache head][row][128] and
-  // log2 of the sum [part][cache head][row].  The drafts are the last part; where one CTA has the
-  // whole window there is one part, theirs, and that CTA joins it
+  // log2 of the sum [part][cache head][row].  The drafts come in as the parts are joined; where one
+  // CTA has the whole window and there are few of them (fold), it takes them itself and keeps
+  // their result as the one part until it joins it
   int32_t parts;
+  bool fold;
   float* part_o;
   float* part_l;
   unsigned* status;
@@ -204,12 +207,12 @@ __device__ __forceinline__ void store_partial(const Params& p, int part, int h, 
   if (with_l) p.part_l[at] = log2l;
 }
 
-// A window's result of row r: a partial where several CTAs share the window, else the output, with
-// what the drafts gave (written by this CTA as the first partial) joined in.
+// A window's result of row r: a partial where it is joined with others, else the output, with what
+// the drafts gave (kept by this CTA as the one partial) joined in.
 __device__ __forceinline__ void store_row(const Params& p, int part, int h, int64_t r, int d, float4 o, float log2l,
                                           bool with_l) {
-  if (p.parts > 1) return store_partial(p, part, h, r, d, o, log2l, with_l);
-  if (p.parents) {
+  if (p.parts > 1 || (p.parents && !p.fold)) return store_partial(p, part, h, r, d, o, log2l, with_l);
+  if (p.fold) {
     const int64_t at = (int64_t)h * p.rows + r;
     const float lt = *(volatile float*)(p.part_l + at);
     const float4 t = *reinterpret_cast<const float4*>(p.part_o + at * kD + d);
@@ -238,70 +241,96 @@ __device__ __forceinline__ int row_position(const Params& p, const int32_t* pare
   return pos;
 }
 
-// The drafts that rows first, first + stride, ... below r1 of cache head h see: themselves and their
-// ancestors, for this warp, a lane holding 4 dims, in FP32.  A draft that a row does not see is
-// never read for it, so whatever it holds (NaN, Inf) cannot reach the row.  list: kMaxTreeDrafts
-// entries of this warp.
+// Running softmax of one row, four dims a lane: maximum and sum in log2 units, O not normalised.
+struct RowSum {
+  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // Makes `top` (not -inf) the maximum; a NaN of either stays.
+  __device__ __forceinline__ void raise(float top) {
+    top = top != top || m != m ? NAN : fmaxf(m, top);
+    const float a = ex2(m - top);
+    l *= a;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] *= a;
+    m = top;
+  }
+  __device__ __forceinline__ void add(float w, float4 v) {
+    l += w;
+    o[0] = fmaf(w, v.x, o[0]);
+    o[1] = fmaf(w, v.y, o[1]);
+    o[2] = fmaf(w, v.z, o[2]);
+    o[3] = fmaf(w, v.w, o[3]);
+  }
+};
+
+// A draft and its ancestors, one thread: list[0] = i, list[1] its parent, ...; returns their number.
+__device__ __forceinline__ int ancestors_of(const Params& p, const int32_t* parents, int i, int16_t* list) {
+  int n = 0;
+  for (int j = i; j >= 0; j = parent_of(p, parents, j)) list[n++] = (int16_t)j;
+  return n;
+}
+
+// Entries first, first + step, ... of a draft's list (itself and its ancestors) into its row's sum:
+// one warp, a lane holding 4 dims, in FP32.  A draft that a row does not see is never read for it,
+// so whatever it holds (NaN, Inf) cannot reach the row.
+__device__ __forceinline__ void tree_row(const Params& p, const int16_t* list, int n, int first, int step, int i,
+                                         int h, int head, RowSum& row) {
+  constexpr int kBatch = 4;  // reads of this many drafts together
+  const int lane = threadIdx.x & 31;
+  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
+  const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
+  const float slope = p.slopes ? p.slopes[head] : 0.0f;
+  for (int e0 = first; e0 < n; e0 += kBatch * step) {
+    uint2 kw[kBatch], vw[kBatch];
+    float s[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int at = e0 + e * step < n ? e0 + e * step : e0;
+      const int64_t off = (int64_t)list[at] * p.new_pitch + ((int64_t)h * kD + 4 * lane) * 2;
+      kw[e] = *reinterpret_cast<const uint2*>(p.k_new + off);
+      vw[e] = *reinterpret_cast<const uint2*>(p.v_new + off);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
+      s[e] *= p.scale;
+      if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
+      // the list holds draft i, its parent, ...: an entry is its number of positions before i
+      const int back = e0 + e * step;
+      s[e] = (s[e] - slope * (float)back) * kLog2e;
+      if (back >= n || (p.window && back >= p.window)) s[e] = -INFINITY;
+      top = s[e] != s[e] || top != top ? NAN : fmaxf(top, s[e]);
+    }
+    if (top == -INFINITY) continue;
+    row.raise(top);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (s[e] == -INFINITY) continue;
+      row.add(ex2(s[e] - row.m), make_float4(bf16_lo(vw[e].x), bf16_hi(vw[e].x), bf16_lo(vw[e].y), bf16_hi(vw[e].y)));
+    }
+  }
+}
+
+// The drafts that rows first, first + stride, ... below r1 of cache head h see, for this warp, as
+// partial results.  list: kMaxFoldedDrafts entries of this warp.
 __device__ __forceinline__ void tree_rows(const Params& p, const int32_t* parents, int16_t* list, int h,
                                           int64_t first, int64_t r1, int stride) {
   const int lane = threadIdx.x & 31;
-  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
   for (int64_t r = first; r < r1 && r < p.rows; r += stride) {
-    const int i = (int)(p.by_group.div((uint32_t)r));
+    const int i = (int)p.by_group.div((uint32_t)r);
     const int head = h * p.group + (int)(r - (int64_t)i * p.group);
     int n = 0;
-    if (lane == 0)
-      for (int j = i; j >= 0; j = parent_of(p, parents, j)) list[n++] = (int16_t)j;
+    if (lane == 0) n = ancestors_of(p, parents, i, list);
     n = __shfl_sync(0xFFFFFFFFu, n, 0);
     __syncwarp();
-    const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
-    const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-    const float slope = p.slopes ? p.slopes[head] : 0.0f;
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int e0 = 0; e0 < n; e0 += 4) {
-      uint2 kw[4], vw[4];
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = e0 + e < n ? e0 + e : e0;
-        const int64_t off = (int64_t)list[at] * p.new_pitch + ((int64_t)h * kD + 4 * lane) * 2;
-        kw[e] = *reinterpret_cast<const uint2*>(p.k_new + off);
-        vw[e] = *reinterpret_cast<const uint2*>(p.v_new + off);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
-        s[e] *= p.scale;
-        if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
-        // the list holds draft i, its parent, ...: entry e0 + e is that many positions before it
-        s[e] = (s[e] - slope * (float)(e0 + e)) * kLog2e;
-        if (e0 + e >= n || (p.window && e0 + e >= p.window)) s[e] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-      if (s[0] != s[0] || s[1] != s[1] || s[2] != s[2] || s[3] != s[3]) top = NAN;
-      if (top == -INFINITY) continue;
-      top = top != top ? top : fmaxf(m, top);
-      const float a = ex2(m - top);
-      l *= a;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] *= a;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (s[e] == -INFINITY) continue;
-        const float w = ex2(s[e] - top);
-        l += w;
-        o[0] = fmaf(w, bf16_lo(vw[e].x), o[0]);
-        o[1] = fmaf(w, bf16_hi(vw[e].x), o[1]);
-        o[2] = fmaf(w, bf16_lo(vw[e].y), o[2]);
-        o[3] = fmaf(w, bf16_hi(vw[e].y), o[3]);
-      }
-      m = top;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    store_partial(p, p.parts - 1, h, r, 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
-                  l == 0.0f ? -INFINITY : m + log2f(l), lane == 0);
+    RowSum row;
+    tree_row(p, list, n, 0, 1, i, h, head, row);
+    const float inv = row.l > 0.0f ? 1.0f / row.l : (row.l == 0.0f ? 0.0f : row.l);
+    store_partial(p, 0, h, r, 4 * lane, make_float4(row.o[0] * inv, row.o[1] * inv, row.o[2] * inv, row.o[3] * inv),
+                  row.l == 0.0f ? -INFINITY : row.m + log2f(row.l), lane == 0);
     __syncwarp();
   }
 }

@@ -58,11 +58,8 @@ struct Control {
 };
 constexpr int kControlBytes = (sizeof(Control) + 127) / 128 * 128;
 
-// parents and, for the two warps that follow them, lists of ancestors
-constexpr int kTreeBytes = kMaxTreeDrafts * 4 + 2 * kMaxTreeDrafts * 2;
-
 constexpr int smem_bytes(bool pair) {
-  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 8 + kTreeBytes;
+  return 1024 + (pair ? 2 : 1) * kQBytes + 2 * kStages * kKvBytes + kControlBytes + kMaxListed * 8 + kMaxTreeDrafts * 4;
 }
 
 // Instruction descriptor: D FP32 (bits 4..5 = 1), A and B binary16 (0), N >> 3, M >> 4; bit 16: B
@@ -157,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 
   pdl_wait();
   int32_t* parents = reinterpret_cast<int32_t*>(list + kMaxListed);
-  if (p.parents) {
+  if (p.parents && positions) {
     for (int i = threadIdx.x; i < p.drafts; i += kThreads) parents[i] = p.parents[i];
     __syncthreads();
   }
@@ -378,16 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       }
       commit(smem_u32(&ct.done[t]));
       mbar_wait_drain(smem_u32(&ct.done[t]), 0, kWaitNs);
-    }
-    // the issuing warps' neighbours take the drafts that the rows see among themselves, each CTA of
-    // the window's split its share of the rows
-    if (p.parents && t >= 2) {
-      int16_t* ancestors = reinterpret_cast<int16_t*>(parents + kMaxTreeDrafts) + (t - 2) * kMaxTreeDrafts;
-      tree_rows(p, parents, ancestors, h, r0 + 2 * part + (t - 2), r_end, 2 * p.splits);
-      if (p.parts == 1) {  // the softmax warps of this CTA join them
-        __threadfence_block();
-        asm volatile("bar.arrive 2, 320;" ::: "memory");
-      }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
@@ -662,7 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     }
     fence_after();
     {  // after a wait that gave up as well: every softmax warp meets at the barrier below
-      if (p.parents && p.parts == 1) asm volatile("bar.sync 2, 320;" ::: "memory");
       float other = 0.0f;  // factor of tile 1's output, when the two are joined
       float mine = 1.0f;
       if (!kPair) {

@@ -13,6 +13,7 @@ namespace {
 using tc::smem_u32;
 
 constexpr int kRows = 16;       // most query rows of a cache head that a CTA takes
+constexpr int64_t kMostRows = 64;  // and that are dealt out to such CTAs
 constexpr int kStep = 32;       // keys a warp takes at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int part = blockIdx.x, h = blockIdx.y;
+  const int64_t r0 = (int64_t)blockIdx.z * kRows, last_row = p.rows - 1;
   const bool positions = p.causal || p.window || p.prefix || p.slopes;
   if (p.parents && (p.fold || positions)) {
     for (int i = threadIdx.x; i < p.drafts; i += kThreads) sh.tree.parents[i] = p.parents[i];
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   int q_first = 0, q_last = 0;
   if (positions || p.parents || (kExtras && p.q_doc)) {
     if (threadIdx.x < kRows) {
-      const int r = (int)min((int64_t)threadIdx.x, p.rows - 1);
+      const int64_t r = min(r0 + threadIdx.x, last_row);
       sh.row_pos[threadIdx.x] = positions ? row_position(p, sh.tree.parents, r) : 0;
       if (kExtras) sh.row_doc[threadIdx.x] = p.q_doc ? p.q_doc[p.by_group.div((uint32_t)r)] : 0;
     }
@@ -163,15 +165,15 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   };
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) issue(i);
-  if (warp == kWarps - 1) load_slots(p, sh.view, &sh.gv_top, part == 0 && h == 0);
+  if (warp == kWarps - 1) load_slots(p, sh.view, &sh.gv_top, part == 0 && h == 0 && r0 == 0);
 
   // queries as binary16 B fragments: lane (g, c) holds dims 32 c .. of row 8 tile + g
   uint32_t qb[kTiles][8][2];
 #pragma unroll
   for (int u = 0; u < kTiles; ++u) {
-    const int r = (int)min((int64_t)(8 * u + g), p.rows - 1);
-    const int i = (int)p.by_group.div((uint32_t)r);
-    const int head = h * p.group + (r - i * p.group);
+    const uint32_t r = (uint32_t)min(r0 + 8 * u + g, last_row);
+    const int i = (int)p.by_group.div(r);
+    const int head = h * p.group + (int)(r - (uint32_t)i * p.group);
     const uint8_t* src = p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 32 * c) * 2;
     uint32_t w[16];
     unsigned top = 0;
@@ -214,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   for (int u = 0; u < kTiles; ++u) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = (int)min((int64_t)(8 * u + 2 * c + e), p.rows - 1);
+      const uint32_t r = (uint32_t)min(r0 + 8 * u + 2 * c + e, last_row);
       qpos[u][e] = positions ? sh.row_pos[8 * u + 2 * c + e] : 0;
       slope[u][e] = 0.0f;
       if (kExtras && p.slopes)
-        slope[u][e] = kLog2e * p.slopes[h * p.group + (r - (int)p.by_group.div((uint32_t)r) * p.group)];
+        slope[u][e] = kLog2e * p.slopes[h * p.group + (int)(r - p.by_group.div(r) * p.group)];
     }
   }
   int seg_at = -1;
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
             make_float4(o[u][j][k], o[u][j + 1][k], o[u][j + 2][k], o[u][j + 3][k]);
   }
   __syncthreads();
-  for (int r = warp; r < 8 * kTiles && r < p.rows; r += kWarps) {
+  for (int r = warp; r < 8 * kTiles && r0 + r < p.rows; r += kWarps) {
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.join.m[w][r]);
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
       acc.w = fmaf(f, v.w, acc.w);
     }
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum * sh.gv_top;
-    store_row(p, part, h, r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
+    store_row(p, part, h, r0 + r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
               sum == 0.0f ? -INFINITY : top + log2f(sum) - kUp, lane == 0);
   }
 }
@@ -604,45 +606,50 @@ struct Plan {
   int32_t splits;       // CTAs that share a window
 };
 
-// Up to 16 rows a cache head take CTAs of few rows, more take tiles of 128 rows.  Either way a
-// window is split over CTAs where that pays: the least of a model of the time, with constants
-// measured on B200 (us): a step of 32 keys takes a warp 1.8 alone and 0.12 more for each warp on its
-// SM; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, and a CTA 9 besides; joining
-// costs a second launch, 5, and the partial results' traffic.
+// Up to kRows rows a cache head take CTAs of few rows, above kMostRows tiles of 128; in between, where
+// CTAs of few rows decode the window more than once but start sooner, and for the number of CTAs
+// that share a window, the least of a model of the time decides, with constants measured on B200
+// (us): a step of 32 keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its
+// SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
+// besides; joining is another launch, 5, the partial results' traffic and 0.04 a part.
 Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
-  Plan plan;
-  plan.tiles = rows > kRows;
-  plan.step = plan.tiles ? kTileKeys : kStep;
-  int64_t steps = 0;
-  for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + plan.step - 1) / plan.step;
-  plan.steps = (int32_t)steps;
-  int64_t splits = 1;
-  double best = 0.0;
-  auto consider = [&](int64_t n, double us) {
-    if (n > 1) us += 5.0 + 2.0 * n * heads * rows * 516 / 5e6;
-    if (best == 0.0 || us < best) {
-      best = us;
-      splits = n;
-    }
-  };
-  if (!plan.tiles) {
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / heads, steps / kWarps));
-    for (int64_t n = 1; n <= most; ++n) {
-      const int64_t mine = (steps + n * kWarps - 1) / (n * kWarps);
-      consider(n, mine * (1.8 + 0.12 * kWarps * n * heads / kSms));
-    }
-  } else {
+  Plan best = {};
+  double best_us = 0.0;
+  rows = std::max<int64_t>(rows, 1);
+  for (int tiles = rows > kMostRows; tiles <= (rows > kRows ? 1 : 0); ++tiles) {
+    Plan plan;
+    plan.tiles = tiles != 0;
+    plan.step = plan.tiles ? kTileKeys : kStep;
+    int64_t steps = 0;
+    for (int i = 0; i < n_slots; ++i) steps += (tokens[i] + plan.step - 1) / plan.step;
+    plan.steps = (int32_t)steps;
     const bool pair = rows > kTileRows;
-    const int64_t base = heads * ((rows + (pair ? 2 : 1) * kTileRows - 1) / ((pair ? 2 : 1) * kTileRows));
-    const int64_t least = std::max<int64_t>((steps + kMaxListed - 1) / kMaxListed, 1);
-    const int64_t most = std::max<int64_t>(least, std::min<int64_t>(steps / 4, kSms));
-    for (int64_t n = least; n <= most; ++n) {
-      const int64_t waves = (base * n + kSms - 1) / kSms;
-      consider(n, waves * ((steps + n - 1) / n * (pair ? 1.2 : 0.65) + 9.0));
+    const int64_t at_once = !plan.tiles ? kRows : pair ? 2 * kTileRows : kTileRows;
+    const int64_t base = heads * ((rows + at_once - 1) / at_once);
+    int64_t least = 1, most;
+    if (plan.tiles) {
+      least = std::max<int64_t>((steps + kMaxListed - 1) / kMaxListed, 1);
+      most = std::min<int64_t>(steps / 4, kSms);
+    } else {
+      most = std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / base, steps / kWarps);
+    }
+    for (int64_t n = least; n <= std::max(least, most); ++n) {
+      double us;
+      if (plan.tiles) {
+        us = (double)((base * n + kSms - 1) / kSms) * ((double)((steps + n - 1) / n) * (pair ? 1.2 : 0.65) + 14.0);
+      } else {
+        const double warps = (double)(kWarps * n * base) / kSms;  // on an SM
+        us = (double)((steps + n * kWarps - 1) / (n * kWarps)) * (rows <= 8 ? 1.8 + 0.12 * warps : 2.2 + 0.18 * warps) + 5.0;
+      }
+      if (n > 1) us += 5.0 + 0.04 * n + 2.0 * n * heads * rows * 516 / 5e6;
+      if (best_us == 0.0 || us < best_us) {
+        best_us = us;
+        best = plan;
+        best.splits = (int32_t)n;
+      }
     }
   }
-  plan.splits = (int32_t)splits;
-  return plan;
+  return best;
 }
 
 template <bool kExtras, int kTiles>
@@ -728,7 +735,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     p.part_o = a.workspace;
     p.part_l = a.workspace + (int64_t)p.parts * p.heads * p.rows * kD;
   }
-  const dim3 grid(p.parts, p.heads);
+  const dim3 grid(p.parts, p.heads, (unsigned)((p.rows + kRows - 1) / kRows));  // of CTAs of few rows
   cudaError_t e;
   if (plan.tiles) e = launch_attend_tiles(p, s);
   else if (p.cap > 0.0f || p.slopes || p.k_doc)

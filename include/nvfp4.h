@@ -460,8 +460,8 @@ nvfp4_status kv_tree_attention(const nvfp4_kv_cache* cache, const int32_t* slots
  *   weight   : device [cols] of wt (NVFP4_BF16 or NVFP4_FP32), 16-byte aligned; NULL = ones.
  *   eps      : finite, >= 0.
  *   gscale_in, out, amax_out : as for nvfp4_quantize, with y in x's place.  A supplied
- *              scale takes one pass over x; without one amax_out is required and h is
- *              read a second time.
+ *              scale (it may be *out->gscale) takes one pass over x; without one amax_out
+ *              is required and h is read a second time.  amax_out is neither of the two.
  * Device status NONFINITE if y holds a NaN or Inf: without gscale_in codes, scales and
  * *out->gscale are then not written, with it they are unspecified.  Errors: INVALID_ARG,
  * SHAPE (cols % 16, mismatched rows/cols, pitch below cols), ALIGNMENT. */

@@ -632,6 +632,8 @@ nvfp4_status nvfp4_rmsnorm_quantize(const void* x, int32_t xt, int64_t rows, int
   if (out->rows != rows || out->cols != cols) return NVFP4_ERR_SHAPE;
   if (rows > 0 && (ldx < cols || (residual && ldr < cols) || (h_out && ldh < cols))) return NVFP4_ERR_SHAPE;
   if (!gscale_in && !amax_out) return NVFP4_ERR_INVALID_ARG;
+  // max|y| is written while the scales are still read
+  if (amax_out && (amax_out == gscale_in || amax_out == out->gscale)) return NVFP4_ERR_INVALID_ARG;
   const int64_t esz = xt == NVFP4_BF16 ? 2 : 4;
   if (rows > 0 && (!aligned16(x) || !aligned16(residual) || !aligned16(h_out) || (ldx * esz) % 16 != 0 ||
                    (residual && (ldr * esz) % 16 != 0) || (h_out && (ldh * esz) % 16 != 0)))

@@ -39,6 +39,8 @@ def test_rmsnorm_refusals():
     assert _norm(w=A) == nv.ERR_ALIGNMENT
     assert _norm(ldx=68) == nv.ERR_ALIGNMENT
     assert _norm(res=P, ldr=66) == nv.ERR_ALIGNMENT
+    assert _norm(amax=P) == nv.ERR_INVALID_ARG  # max|y| over a scale that is still read
+    assert _norm(g=ctypes.c_void_p(8192), amax=ctypes.c_void_p(8192)) == nv.ERR_INVALID_ARG
     # in place with another pitch: rows would overwrite one another
     assert _norm(h=P, ldh=72) == nv.ERR_INVALID_ARG
     bad = _tensor(cols=64)

@@ -471,7 +471,8 @@ nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int
     if (tokens_host[i] < 1 || tokens_host[i] > cache->chunk_tokens) return NVFP4_ERR_SHAPE;
   if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0) return NVFP4_ERR_SHAPE;
   if (tq > nvfp4::kMaxAttentionRows / (q_heads / cache->heads)) return NVFP4_ERR_SHAPE;
-  *bytes = nvfp4::attention_workspace_bytes(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
+  *bytes =
+      nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads)).workspace_bytes;
   return NVFP4_OK;
 }
 
@@ -510,9 +511,8 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   }
   unsigned* status = nullptr;
   if (tq == 0) return current_device(&status);
-  const size_t need =
-      nvfp4::attention_workspace_bytes(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
-  if (!at->workspace || at->workspace_bytes < need) return NVFP4_ERR_INVALID_ARG;
+  a.plan = nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
+  if (!at->workspace || at->workspace_bytes < a.plan.workspace_bytes) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(at->workspace)) return NVFP4_ERR_ALIGNMENT;
   if ((st = current_device(&status)) != NVFP4_OK) return st;
   a.cache = &L;

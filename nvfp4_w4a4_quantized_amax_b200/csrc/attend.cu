@@ -600,24 +600,17 @@ __global__ void __launch_bounds__(256) attend_join_tree_kernel(const __grid_cons
 
 constexpr int kSms = 148;
 
-struct Plan {
-  bool tiles;           // tensor-core form for many rows, else 16-row CTAs
-  int32_t step, steps;  // keys a step, steps in the window (none straddles two slots)
-  int32_t splits;       // CTAs that share a window
-};
-
 // Up to kRows rows a cache head take CTAs of few rows, above kMostRows tiles of 128; in between, where
 // CTAs of few rows decode the window more than once but start sooner, and for the number of CTAs
 // that share a window, the least of a model of the time decides, with constants measured on B200
 // (us): a step of 32 keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its
 // SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
 // besides; joining is another launch, 5, the partial results' traffic and 0.04 a part.
-Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
-  Plan best = {};
+AttentionPlan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+  AttentionPlan best = {};
   double best_us = 0.0;
-  rows = std::max<int64_t>(rows, 1);
   for (int tiles = rows > kMostRows; tiles <= (rows > kRows ? 1 : 0); ++tiles) {
-    Plan plan;
+    AttentionPlan plan = {};
     plan.tiles = tiles != 0;
     plan.step = plan.tiles ? kTileKeys : kStep;
     int64_t steps = 0;
@@ -633,7 +626,9 @@ Plan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
     } else {
       most = std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / base, steps / kWarps);
     }
-    for (int64_t n = least; n <= std::max(least, most); ++n) {
+    most = std::max(least, most);
+    // every number of CTAs up to 32, then an eighth more at a time
+    for (int64_t n = least; n <= most; n = n == most ? n + 1 : std::min(n + 1 + (n > 32 ? n / 8 : 0), most)) {
       double us;
       if (plan.tiles) {
         us = (double)((base * n + kSms - 1) / kSms) * ((double)((steps + n - 1) / n) * (pair ? 1.2 : 0.65) + 14.0);
@@ -670,9 +665,10 @@ cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
 }  // namespace
 }  // namespace attend
 
-size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
-  const attend::Plan plan = attend::make_plan(tokens, n_slots, heads, rows);
-  return (size_t)plan.splits * heads * rows * (attend::kD + 1) * sizeof(float);
+AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+  AttentionPlan plan = attend::make_plan(tokens, n_slots, heads, std::max<int64_t>(rows, 1));
+  plan.workspace_bytes = (size_t)plan.splits * heads * rows * (attend::kD + 1) * sizeof(float);
+  return plan;
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
@@ -696,7 +692,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.by_group = FastDiv((uint32_t)p.group);
   p.n_slots = a.n_slots;
   p.rows = a.tq * p.group;
-  const Plan plan = make_plan(a.tokens, a.n_slots, c.heads, p.rows);
+  const AttentionPlan& plan = a.plan;
   int32_t steps = 0;
   for (int i = 0; i < a.n_slots; ++i) {
     p.slots[i] = a.slots[i];

@@ -128,7 +128,16 @@ cudaError_t launch_kv_context(const KVLayout& c, const int32_t* slots, const int
 // (parents != nullptr: tq drafts).
 constexpr int kMaxTreeDrafts = 1024;
 constexpr int64_t kMaxAttentionRows = 65535 * 128;  // tq * q_heads / heads
+// How a window is shared out (see make_plan), and the workspace that takes.
+struct AttentionPlan {
+  bool tiles;           // tensor-core form for many rows, else CTAs of few rows
+  int32_t step, steps;  // keys a step, steps in the window (none straddles two slots)
+  int32_t splits;       // CTAs that share a window
+  size_t workspace_bytes;
+};
+AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t rows);
 struct AttentionArgs {
+  AttentionPlan plan;
   const KVLayout* cache;
   const int32_t* slots;
   const int32_t* tokens;
@@ -151,10 +160,9 @@ struct AttentionArgs {
   void* o;
   int64_t ldo;
   float* lse;        // nullable [q_heads][tq]
-  float* workspace;  // attention_workspace_bytes
+  float* workspace;  // plan.workspace_bytes
   unsigned* status;
 };
-size_t attention_workspace_bytes(const int32_t* tokens, int n_slots, int heads, int64_t rows);
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
 
 // Test hook of the grid barrier of the one-launch quantization (see

@@ -311,14 +311,17 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
         for (int k = 0; k < 4; ++k) {
           const int e = k & 1;
 #pragma unroll
+          for (int t = 0; t < 2; ++t) s[t][u][k] = fmaf(s[t][u][k], mul[u][e], bias[u][e]);
+          if (kExtras && p.cap > 0.0f) {
+            tanh2(s[0][u][k], s[1][u][k]);
+            mul2(s[0][u][k], s[1][u][k], s[0][u][k], s[1][u][k], cap, cap);
+          }
+#pragma unroll
           for (int t = 0; t < 2; ++t) {
-            float x = fmaf(s[t][u][k], mul[u][e], bias[u][e]);
+            float x = s[t][u][k];
             if (kExtras || si.vis == 1) {
               const int key = 16 * t + 8 * (k >> 1) + tile_key(g);
-              if (kExtras) {
-                if (p.cap > 0.0f) x = softcap(x, cap, 2.0f * kLog2e);
-                if (p.slopes) x = fmaf(-slope[u][e], fabsf((float)(qpos[u][e] - (kp0 + key))), x);
-              }
+              if (kExtras && p.slopes) x = fmaf(-slope[u][e], fabsf((float)(qpos[u][e] - (kp0 + key))), x);
               if (si.vis == 1) {
                 bool see = key < si.n && visible(p, kp0 + key, qpos[u][e]);
                 if (kExtras && p.k_doc) see = see && docs[min(key, si.n - 1)] == sh.row_doc[8 * u + 2 * c + e];

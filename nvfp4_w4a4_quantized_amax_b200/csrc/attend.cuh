@@ -143,17 +143,11 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// x -> cap tanh(x / cap), through tanh z = 1 - 2 / (1 + 2^(2 z log2 e)): absolute error about
-// cap 2^-22 from ex2.approx and rcp.approx, saturating at both ends.
-__device__ __forceinline__ float softcap(float x, float cap, float two_log2e_over_cap) {
-  return cap - 2.0f * cap * rcp_approx(1.0f + ex2(x * two_log2e_over_cap));
-}
-
 // tanh z for |z| <= kTanhNear: z times a polynomial in z^2, interpolated at the Chebyshev nodes of
 // [0, kTanhNear^2] (the series' nearest singularity, z = i pi / 2, is far: five terms are within
 // 2^-23 of tanh).  Scores are mostly well inside their cap, and this runs on the FMA units, two
-// lanes at a time, where softcap takes two of the sixteen special-function results a cycle that
-// the softmax's own exponentials need.
+// lanes at a time, where the form for larger z takes two of the sixteen special-function results a
+// cycle that the softmax's own exponentials need.
 constexpr float kTanhNear = 0.625f;
 __device__ __forceinline__ void tanh_near2(float& a, float& b) {
   float ua, ub, pa = 0.015043356455862522f, pb = pa;
@@ -163,6 +157,18 @@ __device__ __forceinline__ void tanh_near2(float& a, float& b) {
   fma2(pa, pb, pa, pb, ua, ub, -0.33331942558288574f, -0.33331942558288574f);
   fma2(pa, pb, pa, pb, ua, ub, 0.9999998807907104f, 0.9999998807907104f);
   mul2(a, b, a, b, pa, pb);
+}
+
+// tanh z = 1 - 2 / (1 + 2^(2 z log2 e)) beyond kTanhNear, the polynomial inside it: relative error
+// about 2^-21 everywhere.  The first form alone is off by 2^-22 of the cap however small the score,
+// which under a wide cap is more than the score's other roundings.
+__device__ __forceinline__ void tanh2(float& a, float& b) {
+  const float fa = 1.0f - 2.0f * rcp_approx(1.0f + ex2(a * (2.0f * kLog2e)));
+  const float fb = 1.0f - 2.0f * rcp_approx(1.0f + ex2(b * (2.0f * kLog2e)));
+  const bool na = fabsf(a) <= kTanhNear, nb = fabsf(b) <= kTanhNear;
+  tanh_near2(a, b);
+  a = na ? a : fa;
+  b = nb ? b : fb;
 }
 
 // The visibility of keys [k0, k1] (positions) to queries [q0, q1]: 0 none, 1 some, 2 all.
@@ -276,7 +282,6 @@ __device__ __forceinline__ void tree_row(const Params& p, const int16_t* list, i
                                          int h, int head, RowSum& row) {
   constexpr int kBatch = 4;  // reads of this many drafts together
   const int lane = threadIdx.x & 31;
-  const float rcap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
   const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
   const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
   const float slope = p.slopes ? p.slopes[head] : 0.0f;
@@ -297,7 +302,17 @@ __device__ __forceinline__ void tree_row(const Params& p, const int16_t* list, i
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
       s[e] *= p.scale;
-      if (p.cap > 0.0f) s[e] = softcap(s[e], p.cap, rcap);
+    }
+    if (p.cap > 0.0f) {
+#pragma unroll
+      for (int e = 0; e < kBatch; e += 2) {
+        s[e] /= p.cap, s[e + 1] /= p.cap;
+        tanh2(s[e], s[e + 1]);
+        s[e] *= p.cap, s[e + 1] *= p.cap;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
       // the list holds draft i, its parent, ...: an entry is its number of positions before i
       const int back = e0 + e * step;
       s[e] = (s[e] - slope * (float)back) * kLog2e;

@@ -537,8 +537,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
               mul2(s[e], s[e + 1], s[e], s[e + 1], cap, cap);
             }
           } else {
+            // the rarer form 16 scores at a time through their tensor memory: unrolled over all 64 its
+            // code and registers slowed the other paths as well (a bias without a cap by 7 %)
+#pragma unroll 1
+            for (int k = 0; k < kTileKeys; k += 16) {
+              float x[16];
+              uint32_t w[16];
+              ld_x16(si + k, x);
+              ld_wait();
+              ld_tie16(x);
 #pragma unroll
-            for (int e = 0; e < kTileKeys; ++e) s[e] = softcap(s[e], cap, 2.0f * kLog2e);
+              for (int e = 0; e < 16; e += 2) {
+                x[e] = fmaf(x[e], mul, bias), x[e + 1] = fmaf(x[e + 1], mul, bias);
+                tanh2(x[e], x[e + 1]);
+                w[e] = __float_as_uint(x[e] * cap), w[e + 1] = __float_as_uint(x[e + 1] * cap);
+              }
+              st_x16(si + k, w);
+            }
+            st_wait();
+            ld_x32(si, s);
+            ld_x32(si + 32, s + 32);
+            ld_wait();
+            ld_tie(s);
+            ld_tie(s + 32);
           }
         }
         if (kExtras && p.slopes) {

@@ -221,6 +221,46 @@ def test_query_scales(cuda_dev, scale, tq):
     run(cache, [0, 1], [128, 50], queries(tq, 2, 8, scale=scale), scale=-factor)
 
 
+@pytest.mark.parametrize("tq", [1, 12, 200])
+def test_wide_caps(cuda_dev, tq):
+    """A cap far above the scores changes them by a share of themselves, not of the cap: 2^30 is
+    no cap at all to 2^-40, so the uncapped bounds hold."""
+    cache = build(1, 256, [256, 130], 71)
+    q = queries(tq, 1, 5)
+    o, lse = torch.empty_like(q), torch.empty(1, tq, device="cuda")
+    nv.kv_window_attention(cache, [0, 1], [256, 130], q, D ** -0.5, o, lse_out=lse, softcap=2.0 ** 30)
+    k, v = (torch.cat(t) for t in zip(held(cache, 0, 256), held(cache, 1, 130)))
+    assert_close(o, lse, reference(q, k, v, torch.ones(tq, 386, dtype=torch.bool), D ** -0.5))
+    parents = torch.arange(-1, tq - 1, dtype=torch.int32, device="cuda")  # the drafts' own scores
+    kn, vn = queries(tq, 1, 6), queries(tq, 1, 7)
+    nv.kv_tree_attention(cache, [], [], q, kn, vn, parents, D ** -0.5, o, lse_out=lse, softcap=2.0 ** 30)
+    assert_close(o, lse, reference(q, kn.double().cpu(), vn.double().cpu(),
+                                   torch.ones(tq, tq, dtype=torch.bool).tril(), D ** -0.5))
+
+
+@pytest.mark.parametrize("tq", [8, 200])
+def test_cap_of_unlike_rows(cuda_dev, tq):
+    """Rows far below the cap next to a row at it: their error is a share of their own scores (the
+    bound counts 2^-20 of them in place of 2^-20 of the cap)."""
+    cache = build(1, 256, [256], 73)
+    q = queries(tq, 1, 8)
+    q[3] *= 4096
+    cap, seen = 8192.0, torch.ones(tq, 256, dtype=torch.bool)
+    o, lse = torch.empty_like(q), torch.empty(1, tq, device="cuda")
+    nv.kv_window_attention(cache, [0], [256], q, D ** -0.5, o, lse_out=lse, softcap=cap)
+    k, v = held(cache, 0, 256)
+    x = q.double().cpu()[:, 0] @ k[:, 0].T * D ** -0.5
+    small = [i for i in range(tq) if i != 3]
+    assert x[3].abs().max() > cap > 100 * x[small].abs().max()
+    want = torch.logsumexp(cap * torch.tanh(x / cap), -1)
+    err = (2.0 ** -19 * D ** -0.5 * (q.double().cpu()[:, 0].abs() @ k[:, 0].abs().T
+                                      + 4 * q.double().cpu()[:, 0].abs().sum(-1, keepdim=True))
+           + 2.0 ** -20 * x.abs()).amax(-1) + 2.0 ** -20 * (1 + want.abs())
+    assert bool(((lse[0].double().cpu() - want).abs() <= err)[small].all())
+    ref = reference(q, k, v, seen, D ** -0.5, cap)
+    assert_close(o, lse, ref)
+
+
 @pytest.mark.parametrize("tq", [3, 150])
 def test_nonfinite_queries_stay_in_their_rows(cuda_dev, tq):
     cache = build(2, 128, [128, 128], 37)

@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         const int t0 = (int)(st.x - (uint32_t)((int64_t)p.slots[seg_at] * p.chunk));
         const int kp0 = p.pos[seg_at] + t0;
 #pragma unroll
-        for (int e = 0; e < kTileKeys; ++e) s[e] = fmaf(s[e], mul, bias);
+        for (int e = 0; e < kTileKeys; e += 2) fma2(s[e], s[e + 1], s[e], s[e + 1], mul, mul, bias, bias);
         if (kExtras && p.cap > 0.0f) {
           const float cap = p.cap * kLog2e;
           float far = 0.0f;

@@ -407,7 +407,8 @@ typedef struct nvfp4_attention {
 } nvfp4_attention;
 
 /* Workspace of kv_window_attention (tq queries) or kv_tree_attention (tq drafts) over a
- * window of these token counts (HOST array). */
+ * window of these token counts (HOST array).  0 where many queries leave nothing to join:
+ * workspace may then be NULL. */
 nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int32_t* tokens_host, int32_t n_slots,
                                           int64_t tq, int32_t q_heads, size_t* bytes);
 
@@ -417,7 +418,8 @@ nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int
  *              q_heads a multiple of the cache's heads (shared heads).
  *   o_out    : device bf16 [tq][q_heads][128], row pitch ldo elements.
  *   lse_out  : device fp32 [q_heads][tq], nullable.
- * Bases and pitches 16-byte aligned; head_dim 128; tq * q_heads / heads <= 65535 * 128.
+ * Bases and pitches 16-byte aligned; head_dim 128; tq * q_heads / heads <= 65535 * 128;
+ * max_chunks * chunk_tokens < 2^32.
  * A listed slot whose recorded token count differs sets device status NVFP4_ERR_SHAPE and
  * its keys count as masked.  Errors: INVALID_ARG, SHAPE, ALIGNMENT. */
 nvfp4_status kv_window_attention(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,

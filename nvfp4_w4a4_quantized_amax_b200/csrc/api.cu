@@ -471,8 +471,7 @@ nvfp4_status kv_attention_workspace_bytes(const nvfp4_kv_cache* cache, const int
     if (tokens_host[i] < 1 || tokens_host[i] > cache->chunk_tokens) return NVFP4_ERR_SHAPE;
   if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0) return NVFP4_ERR_SHAPE;
   if (tq > nvfp4::kMaxAttentionRows / (q_heads / cache->heads)) return NVFP4_ERR_SHAPE;
-  *bytes =
-      nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads)).workspace_bytes;
+  *bytes = nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq, q_heads / cache->heads).workspace_bytes;
   return NVFP4_OK;
 }
 
@@ -485,7 +484,8 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   nvfp4_status st = check_cache(cache, &L, /*needs_scratch=*/false);
   if (st != NVFP4_OK) return st;
   if (!at || at->reserved != 0 || ((!q || !o_out) && tq > 0)) return NVFP4_ERR_INVALID_ARG;
-  if (cache->head_dim != 128) return NVFP4_ERR_SHAPE;
+  // the kernels number the cache's tokens in 32 bits
+  if (cache->head_dim != 128 || cache->chunk_tokens * cache->max_chunks > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
   int64_t total = 0;
   if ((st = check_window(cache, slots_host, tokens_host, n_slots, min_slots, &total)) != NVFP4_OK) return st;
   if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0 || cache->heads > 65535) return NVFP4_ERR_SHAPE;
@@ -511,8 +511,9 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   }
   unsigned* status = nullptr;
   if (tq == 0) return current_device(&status);
-  a.plan = nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq * (q_heads / cache->heads));
-  if (!at->workspace || at->workspace_bytes < a.plan.workspace_bytes) return NVFP4_ERR_INVALID_ARG;
+  a.plan = nvfp4::plan_attention(tokens_host, n_slots, cache->heads, tq, q_heads / cache->heads);
+  if (at->workspace_bytes < a.plan.workspace_bytes || (!at->workspace && a.plan.workspace_bytes > 0))
+    return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(at->workspace)) return NVFP4_ERR_ALIGNMENT;
   if ((st = current_device(&status)) != NVFP4_OK) return st;
   a.cache = &L;

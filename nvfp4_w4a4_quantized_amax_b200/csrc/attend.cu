@@ -668,9 +668,12 @@ cudaError_t launch_rows(const Params& p, dim3 grid, cudaStream_t s) {
 }  // namespace
 }  // namespace attend
 
-AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
+AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t tq, int64_t group) {
+  const int64_t rows = tq * group;
   AttentionPlan plan = attend::make_plan(tokens, n_slots, heads, std::max<int64_t>(rows, 1));
-  plan.workspace_bytes = (size_t)plan.splits * heads * rows * (attend::kD + 1) * sizeof(float);
+  // a window that is not shared out writes its results at once, unless drafts may have to be joined
+  if (plan.splits > 1 || tq <= kMaxTreeDrafts)
+    plan.workspace_bytes = (size_t)plan.splits * heads * rows * (attend::kD + 1) * sizeof(float);
   return plan;
 }
 

@@ -135,7 +135,7 @@ struct AttentionPlan {
   int32_t splits;       // CTAs that share a window
   size_t workspace_bytes;
 };
-AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t rows);
+AttentionPlan plan_attention(const int32_t* tokens, int n_slots, int heads, int64_t tq, int64_t group);
 struct AttentionArgs {
   AttentionPlan plan;
   const KVLayout* cache;

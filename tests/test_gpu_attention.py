@@ -319,6 +319,12 @@ def test_streams_graphs_and_workspaces(cuda_dev, tq):
         assert torch.equal(o, want) and torch.equal(o2, want2)
 
 
+def test_many_queries_without_workspace(cuda_dev):
+    cache = build(2, 64, [64, 20], 61)
+    assert nv.kv_attention_workspace_bytes(cache, [64, 20], 1500, 4) == 0
+    run(cache, [0, 1], [64, 20], queries(1500, 4, 1), causal=True)
+
+
 def test_no_queries(cuda_dev):
     cache = build(1, 64, [64], 1)
     q = torch.empty(0, 2, D, dtype=torch.bfloat16, device="cuda")

@@ -156,6 +156,10 @@ def test_attention_refusals(tree):
         assert f(slot_pos_host=(ctypes.c_int64 * 2)(*pos)) == nv.ERR_SHAPE
     assert f(workspace=None) == nv.ERR_INVALID_ARG and f(workspace_bytes=16) == nv.ERR_INVALID_ARG
     assert f(workspace=4100) == nv.ERR_ALIGNMENT
+    huge = nv.nvfp4_kv_cache()
+    assert nv.library().nvfp4_kv_cache_init(ctypes.c_void_p(4096), 1 << 41, 1, 128, 1 << 20, 1 << 12,
+                                            ctypes.byref(huge)) == nv.OK
+    assert f(cache=huge, q_heads=2) == nv.ERR_SHAPE  # 2^32 tokens
 
 
 def test_window_attention_refusals():
@@ -184,6 +188,8 @@ def test_workspace_sizes():
     assert need >= 2 * 6 * 129 * 4 and need % 4 == 0
     assert nv.kv_attention_workspace_bytes(cache, [], 1, 2) > 0  # a tree without a window
     assert nv.kv_attention_workspace_bytes(cache, [64], 0, 2) == 0
+    assert nv.kv_attention_workspace_bytes(cache, [64], 1024, 2) > 0
+    assert nv.kv_attention_workspace_bytes(cache, [64], 1 << 20, 2) == 0  # nothing to join
     for tokens, tq, heads in (([65], 1, 2), ([1], -1, 2), ([1], 1, 3)):
         with pytest.raises(nv.Nvfp4Error):
             nv.kv_attention_workspace_bytes(cache, tokens, tq, heads)

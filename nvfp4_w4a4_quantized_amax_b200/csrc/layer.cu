@@ -1,10 +1,12 @@
 // layer.cu — what a transformer layer does between the GEMMs and the KV cache: RMS norm
 // with the residual's addition and NVFP4 output, and rotary positions.  Both move each
 // element once or twice and are bound by HBM.
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -39,7 +41,7 @@ struct NormParams {
   uint8_t* h;          // nullable
   const uint8_t* w;    // nullable
   int64_t x_pitch, res_pitch, h_pitch;  // bytes
-  bool w_bf16;
+  bool w_bf16, h_wide;  // h_wide: rows of h are 32-byte aligned
   int64_t rows, vrows;  // vrows: rows rounded up to the scale layout's tile
   int32_t nb, vnb;      // blocks a row, and with the scale layout's padding
   double inv_cols, eps;
@@ -50,9 +52,12 @@ struct NormParams {
   const float* gscale_in;
   float* gscale_out;
   unsigned* amax;  // nullable with a supplied scale
+  int32_t stages;   // rows on their way to shared memory (kPipe)
   bool amax_store;  // CTA 0 sees every row: it stores the maximum instead of accumulating it
   unsigned* status;
 };
+constexpr int kSms = 148;
+constexpr size_t kRowRingBytes = 220 * 1024;  // of an SM's shared memory, for rows on their way
 
 // 16 values as loaded: 8 words of bf16 pairs or 16 FP32 words.
 template <bool kBf16>
@@ -65,7 +70,24 @@ struct Block {
       w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
     }
   }
-  __device__ __forceinline__ void store(uint8_t* p) const {
+  __device__ __forceinline__ void load_shared(const uint8_t* p) {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * k);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
+  }
+  // wide: p is 32-byte aligned.  A thread's 32 bytes in one access fill whole sectors; two halves
+  // cost the kernel 5 %.
+  __device__ __forceinline__ void store(uint8_t* p, bool wide) const {
+    if (wide) {
+#pragma unroll
+      for (int k = 0; k < (kBf16 ? 8 : 16); k += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 4 * k), "r"(w[k]), "r"(w[k + 1]),
+                     "r"(w[k + 2]), "r"(w[k + 3]), "r"(w[k + 4]), "r"(w[k + 5]), "r"(w[k + 6]), "r"(w[k + 7])
+                     : "memory");
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < (kBf16 ? 2 : 4); ++k)
       stg_v4(p + 16 * k, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
@@ -77,7 +99,11 @@ struct Block {
   __device__ __forceinline__ void add(const Block& o) {  // FP32 sum, rounded to the stream's type
     if (kBf16) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(get(2 * k) + o.get(2 * k), get(2 * k + 1) + o.get(2 * k + 1));
+      for (int k = 0; k < 8; ++k) {
+        float a, b;
+        add2(a, b, get(2 * k), get(2 * k + 1), o.get(2 * k), o.get(2 * k + 1));
+        w[k] = pack_bf16x2(a, b);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(get(k) + o.get(k));
@@ -114,12 +140,18 @@ __device__ __forceinline__ double block_squares(const Block<kBf16>& b) {
   return s0 + s1;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN of either stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // y of one block, and its largest magnitude's bits (a NaN or Inf gives bits >= 0x7F800000).
 template <bool kBf16>
 __device__ __forceinline__ unsigned norm_values(const NormParams& p, const Block<kBf16>& b, int32_t j, float r,
                                                 float (&y)[16]) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) y[k] = b.get(k) * r;
+  for (int k = 0; k < 16; k += 2) mul2(y[k], y[k + 1], b.get(k), b.get(k + 1), r, r);
   if (p.w) {
     if (p.w_bf16) {
       const uint8_t* src = p.w + (int64_t)j * 32;
@@ -129,8 +161,8 @@ __device__ __forceinline__ unsigned norm_values(const NormParams& p, const Block
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          y[8 * q + 2 * k] *= bf16_lo(w[k]);
-          y[8 * q + 2 * k + 1] *= bf16_hi(w[k]);
+          float* v = y + 8 * q + 2 * k;
+          mul2(v[0], v[1], v[0], v[1], bf16_lo(w[k]), bf16_hi(w[k]));
         }
       }
     } else {
@@ -138,17 +170,19 @@ __device__ __forceinline__ unsigned norm_values(const NormParams& p, const Block
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint4 v = ldg_nc_v4_l1(src + 16 * q);
-        y[4 * q] *= __uint_as_float(v.x);
-        y[4 * q + 1] *= __uint_as_float(v.y);
-        y[4 * q + 2] *= __uint_as_float(v.z);
-        y[4 * q + 3] *= __uint_as_float(v.w);
+        float* u = y + 4 * q;
+        mul2(u[0], u[1], u[0], u[1], __uint_as_float(v.x), __uint_as_float(v.y));
+        mul2(u[2], u[3], u[2], u[3], __uint_as_float(v.z), __uint_as_float(v.w));
       }
     }
   }
-  unsigned m = 0;
+  float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(y[k]) & 0x7FFFFFFFu);
-  return m;
+  for (int k = 0; k < 16; k += 2) {
+    m0 = max_nan(m0, fabsf(y[k]));
+    m1 = max_nan(m1, fabsf(y[k + 1]));
+  }
+  return __float_as_uint(max_nan(m0, m1)) & 0x7FFFFFFFu;
 }
 
 template <bool kMma>
@@ -169,26 +203,57 @@ __device__ __forceinline__ void norm_encode(const NormParams& p, int64_t row, in
   p.scales[kMma ? sf_mma_offset(row, j, p.groups) : row * p.ld_scales + j] = (uint8_t)s;
 }
 
-// kLanes threads a row: 8 (rows up to 8 blocks), 32 (up to 128 blocks), or the whole CTA.
-template <int kLanes>
-__device__ __forceinline__ double row_sum(double v, double* red, int warps) {
-#pragma unroll
-  for (int o = (kLanes == 8 ? 4 : 16); o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (kLanes <= 32) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-  for (int w = 0; w < warps; ++w) s += red[w];  // the same order in every thread and pass
-  __syncthreads();
-  return s;
+// Rows of x and residual on their way to shared memory, one bulk copy each.
+constexpr unsigned long long kRowWaitNs = 2000000000ull;
+constexpr int kMaxStages = 3;
+struct RowRing {
+  uint64_t full[kMaxStages];
+  int abort;
+};
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void fetch_row(const NormParams& p, int64_t row, uint32_t bytes, uint8_t* to,
+                                          uint64_t* bar) {
+  const uint32_t b = tc::smem_u32(bar), dst = tc::smem_u32(to);
+  tc::mbar_arrive_expect_tx(b, 2 * bytes);
+  bulk_load(dst, p.x + row * p.x_pitch, bytes, b);
+  bulk_load(dst + bytes, p.res + row * p.res_pitch, bytes, b);
 }
 
-// Three CTAs of 256 threads an SM (85 registers; two for FP32, whose rows take twice as many): the rows' reads, reduction and encoding follow one
-// another within a CTA, so others have to fill in (8192 x 9216 with residual: two CTAs 122 us, three
-// 107, four 117, five 135).
-template <bool kBf16, bool kMma, int kMode, int kLanes>
+// 1 / sqrt of a row's mean square, from each thread's part of its sum.  kLanes threads a row: 8 (rows
+// up to 8 blocks), 32 (up to 128 blocks), or the whole CTA, whose first warp then takes the root and
+// the quotient for all (both are long in binary64: every warp taking them cost the kernel 1 %).
+template <int kLanes>
+__device__ __forceinline__ float row_factor(const NormParams& p, double v, double* red, float* shared_r) {
+#pragma unroll
+  for (int o = (kLanes == 8 ? 4 : 16); o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (kLanes <= 32) return (float)(1.0 / sqrt(v * p.inv_cols + p.eps));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    double s = red[0];
+    for (int w = 1; w < (int)blockDim.x / 32; ++w) s += red[w];  // the same order in every pass
+    const float r = (float)(1.0 / sqrt(s * p.inv_cols + p.eps));
+    if (threadIdx.x == 0) *shared_r = r;
+  }
+  __syncthreads();
+  return *shared_r;
+}
+
+// Three CTAs of 256 threads an SM (85 registers; two for FP32, whose rows take twice as many): a
+// row's reads, reduction and encoding follow one another within a CTA, so others have to fill in
+// (8192 x 9216 with residual, plain loads: two CTAs 122 us, three 107, four 117, five 135).  Bound by
+// HBM with the encoding's instructions close behind: 90 us for 495 MB (5.5 TB/s; without the encoding
+// 78).
+template <bool kBf16, bool kMma, int kMode, int kLanes, bool kPipe>
 __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParams p) {
+  extern __shared__ __align__(128) uint8_t rows_smem[];
+  __shared__ RowRing ring;
   __shared__ double red[kThreads / 32];
+  __shared__ float shared_r;
   __shared__ unsigned redm[kThreads / 32];
   pdl_trigger();
   pdl_wait();
@@ -215,6 +280,23 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParam
   const bool encodes = kMode != kAmax;
   const int64_t row_end = kMma && encodes ? p.vrows : p.rows;
   unsigned local_max = 0;
+  const uint32_t block_bytes = kBf16 ? 32 : 64, row_bytes = (uint32_t)p.nb * block_bytes;
+  const uint32_t stage_bytes = 2 * row_bytes;
+  auto row_at = [&](int64_t base) { return kMode == kEncode ? row_end - 1 - base : base; };
+  int stage = 0;
+  uint32_t phases = 0;  // bit i: parity of ring place i's next phase
+  if (kPipe) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.stages; ++i) tc::mbar_init(tc::smem_u32(&ring.full[i]), 1);
+      ring.abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      for (int i = 0; i < p.stages; ++i) {
+        const int64_t row = row_at(blockIdx.x + (int64_t)i * gridDim.x);
+        if (row >= 0 && row < p.rows) fetch_row(p, row, row_bytes, rows_smem + i * stage_bytes, &ring.full[i]);
+      }
+    }
+    __syncthreads();
+  }
   // every thread of the CTA takes the same number of steps: the reductions are collective
   for (int64_t base = (int64_t)blockIdx.x * per_cta; base < row_end; base += (int64_t)gridDim.x * per_cta) {
     // the second pass goes backwards: the first one's latest rows are the most likely still in L2
@@ -222,28 +304,59 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParam
     const bool live = row >= 0 && row < p.rows;
     Block<kBf16> kept[kCached];
     double ss = 0.0;
+    if (kPipe) {
+      if (live) {
+        const uint8_t* src = rows_smem + stage * stage_bytes;
+        const uint32_t bar = tc::smem_u32(&ring.full[stage]);
+        if (!__syncthreads_and(tc::mbar_wait(bar, phases >> stage & 1u, &ring.abort, kRowWaitNs))) {
+          if (threadIdx.x == 0) {
+            set_status(p.status, kStatusTimeout);
+            for (int i = 0; i < p.stages; ++i)  // copies still on their way
+              tc::mbar_wait_drain(tc::smem_u32(&ring.full[i]), phases >> i & 1u, kRowWaitNs);
+          }
+          break;
+        }
+        phases ^= 1u << stage;
+#pragma unroll
+        for (int i = 0; i < kCached; ++i) {
+          const int32_t j = lane + i * lanes;
+          if (j < p.nb) {
+            Block<kBf16> r;
+            kept[i].load_shared(src + j * block_bytes);
+            r.load_shared(src + row_bytes + j * block_bytes);
+            kept[i].add(r);
+          }
+        }
+        __syncthreads();  // the row is in registers: its place takes another
+      }
+      if (threadIdx.x == 0) {
+        const int64_t next = row_at(base + (int64_t)p.stages * gridDim.x);
+        if (next >= 0 && next < p.rows)
+          fetch_row(p, next, row_bytes, rows_smem + stage * stage_bytes, &ring.full[stage]);
+      }
+      stage = stage + 1 == p.stages ? 0 : stage + 1;
+    }
     if (live) {
 #pragma unroll
       for (int i = 0; i < kCached; ++i) {
         const int32_t j = lane + i * lanes;
-        if (j < p.nb) kept[i] = norm_input<kBf16, kMode>(p, row, j);
+        if (!kPipe && j < p.nb) kept[i] = norm_input<kBf16, kMode>(p, row, j);
       }
 #pragma unroll
       for (int i = 0; i < kCached; ++i) {
         const int32_t j = lane + i * lanes;
         if (j < p.nb) {
-          if (kMode != kEncode && p.h) kept[i].store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64));
+          if (kMode != kEncode && p.h) kept[i].store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64), p.h_wide);
           ss += block_squares(kept[i]);
         }
       }
       for (int32_t j = lane + kCached * lanes; j < p.nb; j += lanes) {  // rows too wide for the registers
         const Block<kBf16> b = norm_input<kBf16, kMode>(p, row, j);
-        if (kMode != kEncode && p.h) b.store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64));
+        if (kMode != kEncode && p.h) b.store(p.h + row * p.h_pitch + (int64_t)j * (kBf16 ? 32 : 64), p.h_wide);
         ss += block_squares(b);
       }
     }
-    ss = row_sum<kLanes>(ss, red, warps);
-    const float r = (float)(1.0 / sqrt(ss * p.inv_cols + p.eps));
+    const float r = row_factor<kLanes>(p, ss, red, &shared_r);
     if (live) {
 #pragma unroll
       for (int i = 0; i < kCached; ++i) {
@@ -280,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParam
   }
 }
 
-template <bool kBf16, bool kMma, int kMode, int kLanes>
+template <bool kBf16, bool kMma, int kMode, int kLanes, bool kPipe>
 cudaError_t launch_norm_kernel(NormParams p, int threads, cudaStream_t s) {
   const int per_cta = kLanes > 32 ? 1 : threads / kLanes;
   p.amax_store = p.rows <= per_cta;
@@ -290,33 +403,48 @@ cudaError_t launch_norm_kernel(NormParams p, int threads, cudaStream_t s) {
   }
   const int64_t rows = kMma && kMode != kAmax ? p.vrows : p.rows;
   // one wave of CTAs; a row a CTA (or 8 or 32 of them) at a time
-  static std::atomic<int> resident[64][kThreads / 32 + 1];  // per device and CTA size; racing writers agree
-  int dev = 0, wave = 0;
+  static std::atomic<int> resident[64][kThreads / 32 + 1];  // an SM's, per device and CTA size; racing writers agree
+  int dev = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::atomic<int>* known = dev >= 0 && dev < 64 ? &resident[dev][threads / 32] : nullptr;
-  if (known) wave = known->load(std::memory_order_relaxed);
-  if (wave == 0) {
-    int per_sm = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_kernel<kBf16, kMma, kMode, kLanes>, threads, 0);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (known) per_sm = known->load(std::memory_order_relaxed);
+  auto kernel = norm_kernel<kBf16, kMma, kMode, kLanes, kPipe>;
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    if (e == cudaSuccess && kPipe)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowRingBytes);
     if (e != cudaSuccess) return e;
-    wave = per_sm * sms;
-    if (known) known->store(wave, std::memory_order_relaxed);
+    if (known) known->store(per_sm, std::memory_order_relaxed);
   }
-  const int64_t want = (rows + per_cta - 1) / per_cta;
+  size_t smem = 0;
+  if (kPipe) {
+    const size_t stage = (size_t)p.nb * (kBf16 ? 32 : 64) * 2;
+    const size_t fit = kRowRingBytes / per_sm / stage;  // rows, with as many CTAs as registers allow
+    p.stages = (int32_t)std::max<size_t>(std::min<size_t>(fit, kMaxStages), 1);
+    smem = p.stages * stage;
+    per_sm = std::min<int>(per_sm, (int)(kRowRingBytes / smem));
+  }
+  const int64_t want = (rows + per_cta - 1) / per_cta, wave = (int64_t)per_sm * kSms;
   const int grid = (int)(want < wave ? want : wave);
-  return launch_pdl(norm_kernel<kBf16, kMma, kMode, kLanes>, grid, threads, 0, s, p);
+  return launch_pdl(kernel, grid, threads, smem, s, p);
 }
 
 template <bool kBf16, bool kMma, int kMode>
 cudaError_t launch_norm_mode(const NormParams& p, cudaStream_t s) {
-  if (p.nb <= 8) return launch_norm_kernel<kBf16, kMma, kMode, 8>(p, kThreads, s);
-  if (p.nb <= 32 * kCached) return launch_norm_kernel<kBf16, kMma, kMode, 32>(p, kThreads, s);
+  if (p.nb <= 8) return launch_norm_kernel<kBf16, kMma, kMode, 8, false>(p, kThreads, s);
+  if (p.nb <= 32 * kCached) return launch_norm_kernel<kBf16, kMma, kMode, 32, false>(p, kThreads, s);
   // as many threads as share the row's blocks evenly
   const int rounds = (p.nb + kThreads - 1) / kThreads;
   const int threads = ((p.nb + rounds - 1) / rounds + 31) / 32 * 32;
-  return launch_norm_kernel<kBf16, kMma, kMode, kThreads>(p, threads, s);
+  // x and residual through shared memory, the next row's on their way while this one's is encoded:
+  // 8192 x 9216 takes 90 us so and 103 with plain loads, 8192 x 14336 151 and 167.  With x alone the
+  // plain loads keep up (76 and 70), as they do for few rows a CTA (592 x 9216: 11.9 and 11.0) and one
+  // block a thread (2368 x 4096: 20.3 and 20.1).
+  const bool both = p.res && !(kMode == kEncode && p.h);
+  if (both && rounds > 1 && rounds <= kCached && p.rows >= 8 * kSms)
+    return launch_norm_kernel<kBf16, kMma, kMode, kThreads, true>(p, threads, s);
+  return launch_norm_kernel<kBf16, kMma, kMode, kThreads, false>(p, threads, s);
 }
 
 template <bool kBf16, bool kMma>
@@ -507,6 +635,7 @@ cudaError_t launch_rmsnorm_quantize(const RmsnormArgs& a, cudaStream_t s) {
   p.x_pitch = a.ldx * esz;
   p.res_pitch = a.ldr * esz;
   p.h_pitch = a.ldh * esz;
+  p.h_wide = ((reinterpret_cast<uintptr_t>(a.h_out) | (uintptr_t)p.h_pitch) & 31u) == 0;
   p.w_bf16 = a.w_bf16;
   p.rows = a.rows;
   p.nb = (int32_t)(a.cols / 16);

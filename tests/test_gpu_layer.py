@@ -250,3 +250,35 @@ def test_rope_packed_buffer_into_a_chunk(cuda_dev):
     nv.nvfp4_rope(buf[:, :10], t, 100)
     nv.nvfp4_rope(want[:, :8].contiguous(), t, 100)
     assert torch.equal(buf[:, 8:10], dense) and torch.equal(buf[:, 10:], want[:, 10:])
+
+
+@pytest.mark.parametrize("bf16,cols", [(True, 4112), (True, 14336), (False, 5120)])
+@pytest.mark.parametrize("layout", [nv.SF_MMA, nv.SF_ROWMAJOR])
+@pytest.mark.parametrize("h,given", [("new", True), ("new", False), ("none", True), ("none", False), ("res", True),
+                                     ("res", False)])
+def test_norm_many_wide_rows(cuda_dev, bf16, cols, layout, h, given):
+    """Several rows a CTA, x and residual by way of shared memory: the same bits as the norm of their
+    sum, which takes plain loads."""
+    rows = 1203
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, res = (torch.randn(rows, cols, device="cuda", generator=gen).to(dt) for _ in range(2))
+    w = torch.rand(cols, device="cuda", generator=gen).bfloat16()
+    g = torch.full((1,), 0.003, device="cuda") if given else None
+    total = (x.float() + res.float()).to(dt)
+    out = []
+    for residual in (None, res.clone()):
+        q, amax = nv.NVFP4Tensor(rows, cols, sf_layout=layout), torch.zeros(1, device="cuda")
+        q.codes.fill_(0xAA)
+        q.scales.fill_(0xAA)
+        ho = None
+        if residual is not None:
+            ho = {"new": torch.empty_like(x), "none": None, "res": residual}[h]
+        nv.nvfp4_rmsnorm_quantize(total if residual is None else x, q, weight=w, residual=residual, h_out=ho,
+                                  gscale_in=g, amax_out=amax)
+        torch.cuda.synchronize()
+        out.append((q.codes, q.scales, q.gscale, amax))
+    assert device_status() == nv.OK
+    assert ho is None or torch.equal(ho, total)
+    for want, got in zip(*out):
+        assert torch.equal(got, want)

@@ -10,9 +10,10 @@
 // queries enter as binary16 after a power-of-two scaling of each row that puts its largest
 // element in [2^14, 2^15): exact for elements down to 2^-29 of it and within 2^-40 of it
 // below.  The weights enter as binary16 with a row's largest between 2^10 and 2^14: rounded by
-// 2^-11 of their value at most (bf16: 2^-8), or by 2^-35 of the largest where they are small.  g_V differs from slot to slot: relative to the window's
-// largest it goes into the exponent of the weights (see SlotView::lg), and O is multiplied by
-// the largest at the end.  Scores, softmax statistics and sums are FP32.
+// 2^-11 of their value at most (bf16: 2^-8), or by 2^-35 of the largest where they are small.  g_V
+// differs from slot to slot: relative to the window's largest it goes into the exponent of the
+// weights (see SlotView::lg), and O is multiplied by the largest at the end.  Scores, softmax
+// statistics and sums are FP32.
 #pragma once
 
 #include "common.cuh"

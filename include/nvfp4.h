@@ -370,9 +370,10 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
  *   lse[h, i] = ln sum_j exp(s), over the visible keys.  A query that sees no key gets
  * O = 0 and lse = -inf.  O is stored as bf16 (RNE).  Products on the tensor cores in
  * binary16 with FP32 sums: e2m1 * s is exact there, queries are scaled by a power of two
- * a row (exact for elements down to 2^-29 of the row's largest), weights are rounded by
- * at most 2^-11 of their value (2^-35 of the row's largest where they are small); softmax
- * statistics and lse are FP32.  A slot whose g_V is below 2^-60 of the window's largest
+ * a row (exact for elements down to 2^-29 of the row's largest), weights times their
+ * slot's g_V are rounded by at most 2^-11 of their value (2^-35 of the row's largest such
+ * product where they are small: slots whose g_V lie 10^6 apart keep fewer digits of the
+ * small one's part of an output); softmax statistics and lse are FP32.  A slot whose g_V is below 2^-60 of the window's largest
  * counts as zero values.  Non-finite queries propagate into their own rows.
  *   scale    : finite.  softcap: 0 (none) or positive and finite.
  *   slopes   : device fp32 [q_heads], nullable.

@@ -12,7 +12,8 @@
 // below.  The weights enter as binary16 with a row's largest between 2^10 and 2^14: rounded by
 // 2^-11 of their value at most (bf16: 2^-8), or by 2^-35 of the largest where they are small.  g_V
 // differs from slot to slot: relative to the window's largest it goes into the exponent of the
-// weights (see SlotView::lg), and O is multiplied by the largest at the end.  Scores, softmax
+// weights (see SlotView::lg; these bounds are for the weights so scaled), and O is multiplied by
+// the largest at the end.  Scores, softmax
 // statistics and sums are FP32.
 #pragma once
 

@@ -2,6 +2,7 @@
 // drafted tokens of a tree, and the joining of partial results (attend.cuh gives the formulas).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "attend.cuh"
 #include "tc.cuh"
@@ -20,8 +21,7 @@ constexpr int kThreads = 32 * kWarps;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -91,12 +91,14 @@ __device__ __forceinline__ int tile_key(int n) { return (n >> 1) + 4 * (n & 1); 
 // V~^T: lane (g, c) owns dims 16 g .. 16 g + 15 (8 bytes, one scale) of the keys of columns 2 c,
 // 2 c + 1 (and + 8); nibbles of two keys are interleaved before the conversion, which then yields
 // the pairs the product wants.  P^T comes from S^T by one 8 x 8 transpose a tile.
-// 1 query x 24 heads x 32768 keys: 47 us and the join 4 (2.2 TB/s of the cache's 113 MB).  The copies
-// alone take 31 to 35: a head's codes are 64-byte pieces, which reach 3.6 TB/s.  The rest is the
-// decoding at four warps a scheduler; a CTA of four neighbouring heads (256-byte pieces) took 41, but
-// its 98 parts 16 to join.
+// A loop step takes the scores of one step of keys and the output of the step before: one alone
+// leaves a scheduler's three or four warps waiting for their own latencies.  That takes registers, so
+// three CTAs an SM (168) and not four: 1 query x 24 heads x 32768 keys 44 us with the join, 50 with
+// one step at a time and four CTAs, 51 with both in 128 registers (two CTAs and not three for 16 rows:
+// 16 x 8 heads x 16384 keys 22 and 26).  Bound by the copies and the decoding together: the copies
+// alone take 31 to 35, half as much again as their codes without the 8-byte pieces of scales.
 template <bool kExtras, int kTiles>  // kExtras: a cap, a bias or documents
-__global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
   pdl_trigger();
@@ -229,17 +231,102 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
   }
   int seg_at = -1;
   float lg = 0.0f, inv = 1.0f;
-  bool vzero = false;
+  // S^T of a step: element k of [tile t][u] is key 16 t + 8 (k / 2) + tile_key(g), row 8 u + 2 c + k % 2
+  float s[2][kTiles][4];
+  uint32_t pb[2][kTiles][2];  // weights of the step before, and whether its values count
+  uint32_t keep = 0;
+  // The scores of one step and the output of the step before it: two independent chains, which hide
+  // each other's latencies (there are four warps to a scheduler).
+  auto products = [&](const Stage& now, const Stage& before, auto scores, auto output) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint4 kw[2];
+      uint32_t ks2[2][2];
+      if constexpr (decltype(scores)::value) {
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[t][u][k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // keys g and g + 8
+          kw[e] = *reinterpret_cast<const uint4*>(now.k_codes + (64 * t + 32 * e + lane) * 16);
+          const uint32_t kb = *reinterpret_cast<const uint16_t*>(now.k_scales + (16 * t + 8 * e + g) * 8 + 2 * c);
+          ks2[e][0] = e4m3_to_f16x2_bcast(kb & 0xFFu);
+          ks2[e][1] = e4m3_to_f16x2_bcast(kb >> 8);
+        }
+      }
+      uint2 wa[2], wb[2];
+      uint32_t vs2[2];
+      if constexpr (decltype(output)::value) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // keys of columns 2 c, 2 c + 1, and of 8 further
+          const int key = 16 * t + 8 * e + c;  // and key + 4
+          const int off = (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1);
+          wa[e] = *reinterpret_cast<const uint2*>(before.v_codes + key * 64 + off);
+          wb[e] = *reinterpret_cast<const uint2*>(before.v_codes + (key + 4) * 64 + off);
+          const uint32_t pair = (before.v_scales[key * 8 + g] | ((uint32_t)before.v_scales[(key + 4) * 8 + g] << 8)) & keep;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(vs2[e]) : "h"((uint16_t)pair));
+        }
+      }
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        if constexpr (decltype(scores)::value) {
+#pragma unroll
+          for (int w = 2 * odd; w < 2 * odd + 2; ++w) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              e2m1x8_times_scale(w == 0 ? kw[e].x : w == 1 ? kw[e].y : w == 2 ? kw[e].z : kw[e].w, ks2[e][w >> 1], a[e]);
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) {
+              mma_f16(s[t][u], a[0][0], a[1][0], a[0][1], a[1][1], qb[u][2 * w][0], qb[u][2 * w][1]);
+              mma_f16(s[t][u], a[0][2], a[1][2], a[0][3], a[1][3], qb[u][2 * w + 1][0], qb[u][2 * w + 1][1]);
+            }
+          }
+        }
+        if constexpr (decltype(output)::value) {  // even, then odd dims of the lane's block
+          uint32_t a[2][2][4];  // [column pair][8 dims of the block][dim / 2]
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t xa = w ? wa[e].y : wa[e].x, xb = w ? wb[e].y : wb[e].x;
+              const uint32_t both = odd ? ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u)
+                                        : (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
+              e2m1x8_times_scale(both, vs2[e], a[e][w]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u)
+              mma_f16(o[u][2 * k + odd], a[0][0][k], a[0][1][k], a[1][0][k], a[1][1][k], pb[t][u][0], pb[t][u][1]);
+        }
+      }
+    }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  bool begun = false;
   for (int at = 0;; at = at + 1 == kRing ? 0 : at + 1) {
     copy_wait<kRing - 2>();
     __syncwarp();
     const StepInfo si = sh.info[warp][at];
-    if (si.n == 0) break;
-    const Stage& stage = sh.ring[warp][at];
+    const int free = at == 0 ? kRing - 1 : at - 1;  // the step before's place
+    const Stage &now = sh.ring[warp][at], &before = sh.ring[warp][free];
+    if (si.n == 0) {
+      if (begun) products(now, before, No{}, Yes{});
+      break;
+    }
+    if (begun) products(now, before, Yes{}, Yes{});
+    else products(now, before, Yes{}, No{});
+    begun = true;
+    __syncwarp();
+    issue(free);
     if (si.seg != seg_at) {  // the slot's scales, and q . mu of this lane's rows
       seg_at = si.seg;
       const SlotView sv = sh.view[seg_at];
-      lg = sv.lg, inv = sv.inv, vzero = sv.vzero;
+      lg = sv.lg, inv = sv.inv;
       const float4* mu = reinterpret_cast<const float4*>(
           p.base + p.off_mu + (((int64_t)p.slots[seg_at] * p.heads + h) * kD + 32 * c) * 4);
       float acc[kTiles];
@@ -271,37 +358,8 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
         }
       }
     }
+    keep = 0;
     if (sh.view[seg_at].ok) {
-      // S^T: element k of [tile t][u] is key 16 t + 8 (k / 2) + tile_key(g), row 8 u + 2 c + k % 2
-      float s[2][kTiles][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int u = 0; u < kTiles; ++u)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[t][u][k] = 0.0f;
-        uint4 kw[2];
-        uint32_t s2[2][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // keys g and g + 8
-          kw[e] = *reinterpret_cast<const uint4*>(stage.k_codes + (64 * t + 32 * e + lane) * 16);
-          const uint32_t kb = *reinterpret_cast<const uint16_t*>(stage.k_scales + (16 * t + 8 * e + g) * 8 + 2 * c);
-          s2[e][0] = e4m3_to_f16x2_bcast(kb & 0xFFu);
-          s2[e][1] = e4m3_to_f16x2_bcast(kb >> 8);
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a[2][4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            e2m1x8_times_scale(w == 0 ? kw[e].x : w == 1 ? kw[e].y : w == 2 ? kw[e].z : kw[e].w, s2[e][w >> 1], a[e]);
-#pragma unroll
-          for (int u = 0; u < kTiles; ++u) {
-            mma_f16(s[t][u], a[0][0], a[1][0], a[0][1], a[1][1], qb[u][2 * w][0], qb[u][2 * w][1]);
-            mma_f16(s[t][u], a[0][2], a[1][2], a[0][3], a[1][3], qb[u][2 * w + 1][0], qb[u][2 * w + 1][1]);
-          }
-        }
-      }
       const int kp0 = p.pos[seg_at] + si.t0;
       const int32_t* docs = p.k_doc;
       if (kExtras && docs) {
@@ -358,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
         }
       }
       // weights, transposed: columns 2 c, 2 c + 1 of 16 keys of row g
-      uint32_t pb[2][kTiles][2];
 #pragma unroll
       for (int u = 0; u < kTiles; ++u) {
         float ref[2], sum[2] = {0.0f, 0.0f};
@@ -377,44 +434,8 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 4 : 3) attend_rows_ker
 #pragma unroll
         for (int e = 0; e < 2; ++e) l[u][e] = fmaf(sum[e], inv, l[u][e]);
       }
-      if (!vzero) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint2 wa[2], wb[2];
-          uint32_t s2[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // keys of columns 2 c, 2 c + 1, and of 8 further
-            const int key = 16 * t + 8 * e + c;  // and key + 4
-            const int off = (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1);
-            wa[e] = *reinterpret_cast<const uint2*>(stage.v_codes + key * 64 + off);
-            wb[e] = *reinterpret_cast<const uint2*>(stage.v_codes + (key + 4) * 64 + off);
-            const uint32_t pair = stage.v_scales[key * 8 + g] | ((uint32_t)stage.v_scales[(key + 4) * 8 + g] << 8);
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[e]) : "h"((uint16_t)pair));
-          }
-#pragma unroll
-          for (int odd = 0; odd < 2; ++odd) {  // even, then odd dims of the lane's block
-            uint32_t a[2][2][4];  // [column pair][8 dims of the block][dim / 2]
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const uint32_t xa = w ? wa[e].y : wa[e].x, xb = w ? wb[e].y : wb[e].x;
-                const uint32_t both = odd ? ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u)
-                                          : (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
-                e2m1x8_times_scale(both, s2[e], a[e][w]);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int u = 0; u < kTiles; ++u)
-                mma_f16(o[u][2 * k + odd], a[0][0][k], a[0][1][k], a[1][0][k], a[1][1][k], pb[t][u][0], pb[t][u][1]);
-          }
-        }
-      }
+      if (!sh.view[seg_at].vzero) keep = 0xFFFFu;
     }
-    __syncwarp();
-    issue(at == 0 ? kRing - 1 : at - 1);
   }
   copy_wait<0>();
 
@@ -611,8 +632,8 @@ constexpr int kSms = 148;
 
 // Up to kRows rows a cache head take CTAs of few rows, above kMostRows tiles of 128; in between, where
 // CTAs of few rows decode the window more than once but start sooner, and for the number of CTAs
-// that share a window, the least of a model of the time decides, with constants measured on B200
-// (us): a step of 32 keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its
+// that share a window, the least of a model of the time decides, with constants from B200
+// (us, high for few rows, which no choice depends on: 0.7 of them moved no case by 10 %): a step of 32 keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its
 // SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
 // besides; joining is another launch, 5, the partial results' traffic and 0.04 a part.
 AttentionPlan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
@@ -633,7 +654,7 @@ AttentionPlan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t r
       least = std::max<int64_t>((steps + kMaxListed - 1) / kMaxListed, 1);
       most = std::min<int64_t>(steps / 4, kSms);
     } else {
-      most = std::min<int64_t>((rows <= 8 ? 4 : 3) * kSms / base, steps / kWarps);
+      most = std::min<int64_t>((rows <= 8 ? 3 : 2) * kSms / base, steps / kWarps);
     }
     most = std::max(least, most);
     // every number of CTAs up to 32, then an eighth more at a time

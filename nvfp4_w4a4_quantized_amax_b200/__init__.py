@@ -174,12 +174,23 @@ def _check(status: int, where: str):
         raise Nvfp4Error(status, where)
 
 
-def _stream(stream):
+_torch = None  # imported at the first call that needs it (building does not)
+
+
+def _load_torch():
+    global _torch
     import torch
 
+    _torch = torch
+    return torch
+
+
+def _stream(stream):
+    torch = _torch or _load_torch()
+
     if stream is None:  # the raw handle: building a Stream object costs several microseconds a call
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t) -> Optional[ctypes.c_void_p]:
@@ -205,14 +216,14 @@ def _dense(t, name: str):
 
 
 def _bf16(t, name: str):
-    import torch
+    torch = _torch or _load_torch()
 
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: bf16 is required, got {t.dtype}")
 
 
 def _dtype_code(t) -> int:
-    import torch
+    torch = _torch or _load_torch()
 
     if t.dtype == torch.bfloat16:
         return BF16
@@ -428,7 +439,7 @@ _NO_GUARD = contextlib.nullcontext()
 def _together(names: str, *tensors):
     """Every given tensor (None: not given) is on one CUDA device; returns a guard that makes it the
     current one."""
-    import torch
+    torch = _torch or _load_torch()
 
     dev = -1
     for i, t in enumerate(tensors):
@@ -484,7 +495,7 @@ def _pitch(t) -> int:
 
 
 def _scalar(t, name: str):
-    import torch
+    torch = _torch or _load_torch()
 
     if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
         raise ValueError(f"{name}: one float32 value is required")
@@ -527,7 +538,7 @@ def _heads_view(t, name: str):
 
 def _positions(pos, n: int, name: str):
     """(device int32 tensor or None, first position) of an int or an int32 [n] tensor."""
-    import torch
+    torch = _torch or _load_torch()
 
     if isinstance(pos, torch.Tensor):
         if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != n or not pos.is_contiguous():
@@ -563,7 +574,7 @@ def kv_attention_workspace_bytes(cache: KVCache, tokens: Sequence[int], tq: int,
 
 
 def _int32(t, n: int, name: str):
-    import torch
+    torch = _torch or _load_torch()
 
     if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} values is required")
@@ -571,7 +582,7 @@ def _int32(t, n: int, name: str):
 
 def _attend(where, cache, slots, tokens, q, scale, o_out, lse_out, softcap, slopes, slot_pos, q_pos, workspace, stream,
             causal=False, window=0, prefix=0, q_doc=None, k_doc=None, k_new=None, v_new=None, parents=None):
-    import torch
+    torch = _torch or _load_torch()
 
     if len(tokens) != len(slots) or (slot_pos is not None and len(slot_pos) != len(slots)):
         raise ValueError("one token count (and position) per slot")

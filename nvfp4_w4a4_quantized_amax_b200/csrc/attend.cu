@@ -233,7 +233,10 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_ker
   float lg = 0.0f, inv = 1.0f;
   // S^T of a step: element k of [tile t][u] is key 16 t + 8 (k / 2) + tile_key(g), row 8 u + 2 c + k % 2
   float s[2][kTiles][4];
-  uint32_t pb[2][kTiles][2];  // weights of the step before, and whether its values count
+  // weights of the step before, and whether its values count.  A step of a refused slot leaves them as
+  // they are with its values masked to 0, so they are numbers from the start: 0 times an unset
+  // register could be a NaN
+  uint32_t pb[2][kTiles][2] = {};
   uint32_t keep = 0;
   // The scores of one step and the output of the step before it: two independent chains, which hide
   // each other's latencies (there are four warps to a scheduler).

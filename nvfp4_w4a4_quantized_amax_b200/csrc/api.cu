@@ -501,7 +501,7 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   if (at->causal != 0 && at->causal != 1) return NVFP4_ERR_INVALID_ARG;
   if ((at->q_doc == nullptr) != (at->k_doc == nullptr)) return NVFP4_ERR_INVALID_ARG;
   constexpr int64_t kMaxPos = 0x7FFFFFFF;  // positions are int32 on the device
-  if (at->window < 0 || at->prefix < 0 || at->q_pos < 0 || at->q_pos + tq > kMaxPos) return NVFP4_ERR_SHAPE;
+  if (at->window < 0 || at->prefix < 0 || at->q_pos < 0 || at->q_pos > kMaxPos - tq) return NVFP4_ERR_SHAPE;
   int64_t pos[nvfp4::kMaxWindowSlots];
   int64_t next = 0;
   for (int i = 0; i < n_slots; ++i) {

@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         if (!full) {
           // visible: keys [lo, hi) of the step, and those below pre
           int lo = 0, hi = st_n, pre = 0;
-          if (p.causal) hi = (int)min((int64_t)hi, (int64_t)qpos - kp0 + 1);
+          if (p.causal) hi = (int)min((int64_t)hi, max((int64_t)0, (int64_t)qpos - kp0 + 1));
           if (p.window) lo = (int)max((int64_t)0, (int64_t)qpos - kp0 - p.window + 1);
           if (p.prefix > kp0) pre = min(p.prefix - kp0, st_n);
           const int32_t* docs = p.k_doc;

@@ -25,3 +25,16 @@ def test_refused_slots_before_good_ones(cuda_dev, slots, tokens, tq, group):
     assert device_status() == nv.ERR_SHAPE
     k, v = held(cache, 0, 128)
     assert_close(o, lse, reference(q, k, v, torch.ones(tq, 128, dtype=torch.bool), 0.1))
+
+
+@pytest.mark.parametrize("n", [1, 20, 33, 64, 100])
+@pytest.mark.parametrize("tq", [12, 130, 300])
+@pytest.mark.parametrize("kw", [dict(causal=True), dict(causal=True, window=2 ** 31 - 2), dict(window=5)])
+def test_positions_at_both_ends(cuda_dev, n, tq, kw):
+    """Queries at position 0 and at the last one, keys at the last positions: no number that the mask
+    is made of leaves 32 bits."""
+    cache = build(1, 128, [n], 5)
+    pos = torch.zeros(tq, dtype=torch.int32, device="cuda")
+    pos[::2] = 2 ** 31 - 2
+    run(cache, [0], [n], queries(tq, 1, 3), q_pos=pos, slot_pos=[2 ** 31 - 1 - n], **kw)
+    run(cache, [0], [n], queries(tq, 1, 4), q_pos=pos, **kw)

@@ -654,6 +654,8 @@ def kv_tree_attention(cache: KVCache, slots: Sequence[int], tokens: Sequence[int
     if _heads_view(k_new, "k_new") != shape or _heads_view(v_new, "v_new") != shape or (
             shape[0] > 1 and k_new.stride(0) != v_new.stride(0)):
         raise ValueError("k_new, v_new: [drafts, heads, head_dim] of one row pitch is required")
+    if parents is None:
+        raise ValueError("parents: an int32 tensor of each draft's parent is required")
     _int32(parents, shape[0], "parents")
     _attend("kv_tree_attention", cache, slots, tokens, q, scale, o_out, lse_out, softcap, slopes, slot_pos, int(q_pos),
             workspace, stream, window=window, k_new=k_new, v_new=v_new, parents=parents)

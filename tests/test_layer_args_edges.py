@@ -3,9 +3,10 @@ before any device work.  CPU only."""
 import ctypes
 
 import pytest
+import torch
 
 import nvfp4_w4a4_quantized_amax_b200 as nv
-from test_layer_args import _attend
+from test_layer_args import _attend, _cache
 
 
 @pytest.mark.parametrize("tree", [False, True])
@@ -14,3 +15,11 @@ def test_first_query_position_near_the_end_of_int64(tree):
         assert _attend(tree=tree, q_pos=q_pos) == nv.ERR_SHAPE, q_pos  # of three queries
     for pos in ((1 << 63) - 1, 1 << 32):
         assert _attend(tree=tree, slot_pos_host=(ctypes.c_int64 * 2)(0, pos)) == nv.ERR_SHAPE
+
+
+def test_drafts_without_parents():
+    cache = nv.KVCache.__new__(nv.KVCache)
+    cache.handle, cache.heads, cache.head_dim, cache.buffer = _cache(), 2, 128, torch.zeros(1)
+    q, new = torch.zeros(3, 4, 128, dtype=torch.bfloat16), torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="parents"):
+        nv.kv_tree_attention(cache, [0], [64], q, new, new, None, 0.1, torch.zeros_like(q))

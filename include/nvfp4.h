@@ -375,7 +375,9 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
  * product where they are small: slots whose g_V lie 10^6 apart keep fewer digits of the
  * small one's part of an output); softmax statistics and lse are FP32.  A slot whose g_V is below 2^-60 of the window's largest
  * counts as zero values.  Non-finite queries propagate into their own rows.
- *   scale    : finite.  softcap: 0 (none) or positive and finite.
+ *   scale    : finite; scores have to be FP32 numbers.
+ *   softcap  : 0 (none) or positive and finite; caps above 2^64 act as 2^64 (which leaves scores
+ *              below 2^52 as they are), caps below 2^-30 as 2^-30.
  *   slopes   : device fp32 [q_heads], nullable.
  *   causal   : 1: a key is visible where k_pos <= q_pos;  0: everywhere.
  *   window   : 0, or a key is visible where q_pos - k_pos < window.

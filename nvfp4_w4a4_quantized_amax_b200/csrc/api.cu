@@ -526,7 +526,10 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   a.ldq = ldq;
   a.q_heads = q_heads;
   a.scale = at->scale;
-  a.cap = at->softcap;
+  // Scores are formed as shares of the cap, whose factor leaves FP32's normal range under caps of
+  // extreme size.  2^64 changes a score below 2^52 by 2^-25 of it, as any larger cap changes it by less;
+  // under 2^-30 every score is within 2^-30 of 0, as under any smaller cap.
+  a.cap = at->softcap > 0.0f ? fminf(fmaxf(at->softcap, 0x1p-30f), 0x1p64f) : 0.0f;
   a.slopes = at->slopes;
   a.causal = at->causal != 0;
   a.window = at->window < kMaxPos ? at->window : 0;  // as long as all positions: no limit

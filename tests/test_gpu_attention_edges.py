@@ -38,3 +38,48 @@ def test_positions_at_both_ends(cuda_dev, n, tq, kw):
     pos[::2] = 2 ** 31 - 2
     run(cache, [0], [n], queries(tq, 1, 3), q_pos=pos, slot_pos=[2 ** 31 - 1 - n], **kw)
     run(cache, [0], [n], queries(tq, 1, 4), q_pos=pos, **kw)
+
+
+@pytest.mark.parametrize("cap", [2.0 ** 60, 2.0 ** 110, 2.0 ** 120, 2.0 ** 127, 3.4e38])
+@pytest.mark.parametrize("tq", [1, 12, 200])
+def test_caps_beyond_every_score(cuda_dev, cap, tq):
+    """tanh changes a score of at most 2^9 by less than 2^-100 of it under these caps: the uncapped
+    bounds hold, for keys of the window and for drafts."""
+    cache = build(1, 256, [256, 130], 71)
+    q = queries(tq, 1, 5)
+    o, lse = torch.empty_like(q), torch.empty(1, tq, device="cuda")
+    nv.kv_window_attention(cache, [0, 1], [256, 130], q, D ** -0.5, o, lse_out=lse, softcap=cap)
+    k, v = (torch.cat(t) for t in zip(held(cache, 0, 256), held(cache, 1, 130)))
+    assert_close(o, lse, reference(q, k, v, torch.ones(tq, 386, dtype=torch.bool), D ** -0.5))
+    parents = torch.arange(-1, tq - 1, dtype=torch.int32, device="cuda")
+    kn, vn = queries(tq, 1, 6), queries(tq, 1, 7)
+    nv.kv_tree_attention(cache, [], [], q, kn, vn, parents, D ** -0.5, o, lse_out=lse, softcap=cap)
+    assert_close(o, lse, reference(q, kn.double().cpu(), vn.double().cpu(),
+                                   torch.ones(tq, tq, dtype=torch.bool).tril(), D ** -0.5))
+    assert device_status() == nv.OK
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -30, 2.0 ** -64, 2.0 ** -126, 1e-42])
+@pytest.mark.parametrize("size", [1.5, 2.0 ** 20])
+@pytest.mark.parametrize("tq", [1, 12, 200])
+def test_caps_below_every_score(cuda_dev, cap, size, tq):
+    """Scores within 2^-30 of 0: all weights are one to 2^-29, each rounded to binary16 by at most
+    2^-11, and O to bf16 by 2^-8; lse is the logarithm of the number of keys in FP32."""
+    cache = build(1, 256, [256, 130], 72)
+    q = queries(tq, 1, 5, scale=size)
+    o, lse = torch.empty_like(q), torch.empty(1, tq, device="cuda")
+
+    def check(v, seen):
+        p = seen.double() / seen.sum(-1, keepdim=True)
+        want, tol = p @ v[:, 0], p @ v[:, 0].abs() * 2.0 ** -10
+        assert bool(((o[:, 0].double().cpu() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+        n = seen.sum(-1).double().log()
+        assert bool(((lse[0].double().cpu() - n).abs() <= 2.0 ** -20 * (1 + n)).all())
+
+    nv.kv_window_attention(cache, [0, 1], [256, 130], q, D ** -0.5, o, lse_out=lse, softcap=cap)
+    check(torch.cat([held(cache, 0, 256)[1], held(cache, 1, 130)[1]]), torch.ones(tq, 386, dtype=torch.bool))
+    parents = torch.arange(-1, tq - 1, dtype=torch.int32, device="cuda")
+    kn, vn = queries(tq, 1, 6), queries(tq, 1, 7)
+    nv.kv_tree_attention(cache, [], [], q, kn, vn, parents, D ** -0.5, o, lse_out=lse, softcap=cap)
+    check(vn.double().cpu(), torch.ones(tq, tq, dtype=torch.bool).tril())
+    assert device_status() == nv.OK

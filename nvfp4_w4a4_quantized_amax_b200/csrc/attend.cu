@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_ker
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const int e = query_exponent(top);
     const float up = exp2i(e);
-    if (warp == 0 && c == 0) sh.row_fac[8 * u + g] = p.scale * exp2i(-e);
+    if (warp == 0 && c == 0) sh.row_fac[8 * u + g] = top >= 0x7F80u ? NAN : p.scale * exp2i(-e);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       qb[u][ks][0] = pack_f16x2(bf16_lo(w[2 * ks]) * up, bf16_hi(w[2 * ks]) * up);

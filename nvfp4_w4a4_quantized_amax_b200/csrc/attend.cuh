@@ -125,7 +125,9 @@ __device__ __forceinline__ void load_slots(const Params& p, SlotView* view, floa
 }
 
 // Exponent of the power of two that takes a row of queries with largest magnitude `top` (bf16 bits)
-// to [2^14, 2^15); 0 for a row of zeros, of NaN or Inf (which then reach the output).
+// to [2^14, 2^15); 0 for a row of zeros, or with a NaN or Inf: the whole row (or the factor of its
+// scores) is then NaN, and with it the result wherever it sees a key.  Infinities as they are could give
+// scores of -Inf alone, which look like masked ones, or finite ones under a cap.
 __device__ __forceinline__ int query_exponent(unsigned top) {
   if (top == 0 || top >= 0x7F80u) return 0;
   const int e = 141 - (int)(top >> 7);
@@ -287,6 +289,9 @@ __device__ __forceinline__ void tree_row(const Params& p, const int16_t* list, i
   const uint2 qw = *reinterpret_cast<const uint2*>(p.q + (int64_t)i * p.q_pitch + ((int64_t)head * kD + 4 * lane) * 2);
   const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
   const float slope = p.slopes ? p.slopes[head] : 0.0f;
+  const unsigned top_q = __vmaxu2(qw.x & 0x7FFF7FFFu, qw.y & 0x7FFF7FFFu);
+  const bool odd_q = max(top_q >> 16, top_q & 0xFFFFu) >= 0x7F80u;
+  const float scale = __any_sync(0xFFFFFFFFu, odd_q) ? NAN : p.scale;  // as in the window (query_exponent)
   for (int e0 = first; e0 < n; e0 += kBatch * step) {
     uint2 kw[kBatch], vw[kBatch];
     float s[kBatch];
@@ -303,7 +308,7 @@ __device__ __forceinline__ void tree_row(const Params& p, const int16_t* list, i
       s[e] = fmaf(q[0], bf16_lo(kw[e].x), fmaf(q[1], bf16_hi(kw[e].x), fmaf(q[2], bf16_lo(kw[e].y), q[3] * bf16_hi(kw[e].y))));
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], x);
-      s[e] *= p.scale;
+      s[e] *= scale;
     }
     if (p.cap > 0.0f) {
 #pragma unroll

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
       const int e = query_exponent(top);
       const bool some = r0 + r < r_end;
       // a negative scale goes into the queries, so that larger products are larger scores
-      const float up = copysignf(exp2i(e), p.scale);
+      const float up = copysignf(top >= 0x7F80u ? NAN : exp2i(e), p.scale);
       const uint4 w = make_uint4(pack_f16x2(bf16_lo(v[u].x) * up, bf16_hi(v[u].x) * up),
                                  pack_f16x2(bf16_lo(v[u].y) * up, bf16_hi(v[u].y) * up),
                                  pack_f16x2(bf16_lo(v[u].z) * up, bf16_hi(v[u].z) * up),

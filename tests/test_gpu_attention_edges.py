@@ -83,3 +83,35 @@ def test_caps_below_every_score(cuda_dev, cap, size, tq):
     nv.kv_tree_attention(cache, [], [], q, kn, vn, parents, D ** -0.5, o, lse_out=lse, softcap=cap)
     check(vn.double().cpu(), torch.ones(tq, tq, dtype=torch.bool).tril())
     assert device_status() == nv.OK
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("tq", [2, 12, 100, 200])
+def test_nonfinite_queries_are_nan(cuda_dev, tq, softcap, value):
+    """A query with a NaN or Inf gives NaN where it sees a key, also where all its scores would be
+    -Inf (one visible key) or finite (a cap); it is empty where it sees none; other rows stay."""
+    cache = build(2, 128, [128], 37)
+    q = queries(tq, 2, 1)
+    clean, odd = q.clone(), torch.zeros(tq, dtype=torch.bool, device="cuda")
+    odd[::2] = True
+    q[odd, :, 77] = value
+    o, lse, want = torch.empty_like(q), torch.empty(2, tq, device="cuda"), torch.empty_like(q)
+    for key in range(0, 128, 9):  # the only one that is seen
+        pos = torch.full((tq,), key, dtype=torch.int32, device="cuda")
+        kw = dict(causal=True, window=1, softcap=softcap, q_pos=pos)
+        nv.kv_window_attention(cache, [0], [128], clean, D ** -0.5, want, **kw)
+        nv.kv_window_attention(cache, [0], [128], q, D ** -0.5, o, lse_out=lse, **kw)
+        assert bool(torch.isnan(o[odd]).all()) and bool(torch.isnan(lse[:, odd]).all())
+        assert torch.equal(o[~odd], want[~odd]) and bool(torch.isfinite(lse[:, ~odd]).all())
+    nv.kv_window_attention(cache, [0], [128], q, D ** -0.5, o, lse_out=lse, causal=True, slot_pos=[5000],
+                           softcap=softcap)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    parents = torch.full((tq,), -1, dtype=torch.int32, device="cuda")
+    kn, vn = queries(tq, 2, 6), queries(tq, 2, 7)
+    for slots, tokens in (([], []), ([0], [128])):
+        nv.kv_tree_attention(cache, slots, tokens, clean, kn, vn, parents, D ** -0.5, want, softcap=softcap)
+        nv.kv_tree_attention(cache, slots, tokens, q, kn, vn, parents, D ** -0.5, o, lse_out=lse, softcap=softcap)
+        assert bool(torch.isnan(o[odd]).all()) and bool(torch.isnan(lse[:, odd]).all())
+        assert torch.equal(o[~odd], want[~odd]) and bool(torch.isfinite(lse[:, ~odd]).all())
+    assert device_status() == nv.OK

@@ -504,7 +504,8 @@ nvfp4_status nvfp4_rope_frequencies(int32_t rot_dim, double base, int32_t scalin
  *              way.  Any element alignment; 16-byte aligned bases, pitches, head_dim and
  *              rot_dim (rot_dim / 2 for the half layout) take vector accesses.
  *   freq     : device binary64 [rot_dim / 2];  mscale: finite factor m.
- *   positions: device int32 [tokens], nullable: token t is then at pos0 + t.
+ *   positions: device int32 [tokens], nullable: token t is then at pos0 + t, within +-2^53
+ *              (binary64 angles lose digits beyond 32 bits).
  * 2 <= rot_dim <= head_dim <= 4096, rot_dim even; heads * head_dim <= 2^20.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT.  Non-finite values propagate. */
 nvfp4_status nvfp4_rope(const void* x, int32_t xt, int64_t tokens, int32_t heads, int32_t head_dim, int64_t ldx,

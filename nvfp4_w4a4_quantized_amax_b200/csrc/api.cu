@@ -721,6 +721,7 @@ nvfp4_status nvfp4_rope(const void* x, int32_t xt, int64_t tokens, int32_t heads
   const int64_t width = (int64_t)heads * head_dim;
   if (tokens > (1ll << 31) || width > (1ll << 20)) return NVFP4_ERR_SHAPE;
   if (tokens > 1 && (ldx < width || ldy < width)) return NVFP4_ERR_SHAPE;
+  if (!positions && (pos0 < -(1ll << 53) || pos0 > (1ll << 53) - tokens)) return NVFP4_ERR_SHAPE;  // not binary64 numbers
   const uintptr_t esz = xt == NVFP4_BF16 ? 2 : 4;
   if ((reinterpret_cast<uintptr_t>(x) % esz) || (reinterpret_cast<uintptr_t>(y) % esz) ||
       (reinterpret_cast<uintptr_t>(freq) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))

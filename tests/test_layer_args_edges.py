@@ -23,3 +23,10 @@ def test_drafts_without_parents():
     q, new = torch.zeros(3, 4, 128, dtype=torch.bfloat16), torch.zeros(3, 2, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="parents"):
         nv.kv_tree_attention(cache, [0], [64], q, new, new, None, 0.1, torch.zeros_like(q))
+
+
+def test_first_rope_position_beyond_binary64():
+    P, y = ctypes.c_void_p(4096), ctypes.c_void_p(1 << 20)
+    for pos0 in ((1 << 63) - 1, (1 << 53) - 3, -(1 << 53) - 1, -(1 << 63)):  # of four tokens
+        assert nv.library().nvfp4_rope(P, nv.BF16, 4, 2, 64, 128, P, 64, nv.ROPE_HALF, 1.0, None, pos0, y, 128,
+                                       None) == nv.ERR_SHAPE, pos0

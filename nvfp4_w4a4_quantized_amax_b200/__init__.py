@@ -544,7 +544,10 @@ def _positions(pos, n: int, name: str):
         if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != n or not pos.is_contiguous():
             raise ValueError(f"{name}: an int or a contiguous int32 tensor of {n} positions is required")
         return pos, 0
-    return None, int(pos)
+    first = int(pos)
+    if not -2 ** 63 <= first < 2 ** 63:  # ctypes would keep its low bits
+        raise ValueError(f"{name}: a 64-bit position is required, got {first}")
+    return None, first
 
 
 def nvfp4_rope(x, table: RopeTable, positions=0, y=None, layout: int = ROPE_HALF, stream=None):

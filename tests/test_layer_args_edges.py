@@ -30,3 +30,19 @@ def test_first_rope_position_beyond_binary64():
     for pos0 in ((1 << 63) - 1, (1 << 53) - 3, -(1 << 53) - 1, -(1 << 63)):  # of four tokens
         assert nv.library().nvfp4_rope(P, nv.BF16, 4, 2, 64, 128, P, 64, nv.ROPE_HALF, 1.0, None, pos0, y, 128,
                                        None) == nv.ERR_SHAPE, pos0
+
+
+def test_positions_that_no_c_integer_holds():
+    """Their low 64 bits would be taken for another position."""
+    x, table = torch.zeros(4, 2, 32, dtype=torch.bfloat16), nv.RopeTable(16, device="cpu")
+    cache = nv.KVCache.__new__(nv.KVCache)
+    cache.handle, cache.heads, cache.head_dim, cache.buffer = _cache(), 2, 128, torch.zeros(1)
+    q, new = torch.zeros(3, 4, 128, dtype=torch.bfloat16), torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    parents = torch.full((3,), -1, dtype=torch.int32)
+    for pos in (2 ** 64, 2 ** 63, -2 ** 63 - 1):
+        with pytest.raises(ValueError, match="position"):
+            nv.nvfp4_rope(x, table, pos)
+        with pytest.raises(ValueError, match="position"):
+            nv.kv_window_attention(cache, [0], [64], q, 0.1, torch.zeros_like(q), q_pos=pos)
+        with pytest.raises(ValueError, match="position"):
+            nv.kv_tree_attention(cache, [0], [64], q, new, new, parents, 0.1, torch.zeros_like(q), q_pos=pos)

@@ -479,8 +479,9 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_ker
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum * sh.gv_top;
-    store_row(p, part, h, r0 + r, 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f),
+    // g_V last: the quotient alone is in range, its product with a small g_V need not be
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum, gv = sh.gv_top;
+    store_row(p, part, h, r0 + r, 4 * lane, make_float4(acc.x * f * gv, acc.y * f * gv, acc.z * f * gv, acc.w * f * gv),
               sum == 0.0f ? -INFINITY : top + log2f(sum) - kUp, lane == 0);
   }
 }

@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         }
       }
       if (kPair || tile == 0) {
-        const float f = l == 0.0f ? 0.0f : 1.0f / l * ct.gv_top;
+        // g_V last: the quotient alone is in range, its product with a small g_V need not be
+        const float f = l == 0.0f ? 0.0f : 1.0f / l, gv = ct.gv_top;
         mine *= f;
         other *= f;
         const float log2l = l == 0.0f ? -INFINITY : m + log2f(l) - kUp;
@@ -733,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
               v.z = fmaf(u.z, other, v.z);
               v.w = fmaf(u.w, other, v.w);
             }
+            v.x *= gv, v.y *= gv, v.z *= gv, v.w *= gv;
             if (live) store_row(p, part, h, row, 32 * k + 4 * e, v, log2l, k == 0 && e == 0);
           }
         }

@@ -115,3 +115,19 @@ def test_nonfinite_queries_are_nan(cuda_dev, tq, softcap, value):
         assert bool(torch.isnan(o[odd]).all()) and bool(torch.isnan(lse[:, odd]).all())
         assert torch.equal(o[~odd], want[~odd]) and bool(torch.isfinite(lse[:, ~odd]).all())
     assert device_status() == nv.OK
+
+
+@pytest.mark.parametrize("power", [-80, -105, -117])
+@pytest.mark.parametrize("tq,group", [(1, 1), (5, 2), (100, 1), (300, 1)])
+@pytest.mark.parametrize("scale", [D ** -0.5, 2.0 ** -12])
+def test_small_values(cuda_dev, power, tq, group, scale):
+    """Values whose g_V is close to FP32's smallest numbers keep their digits, with few and with all of
+    the keys counting: in units of 2^power the bounds are the usual ones and bf16's smallest half step,
+    2^-134."""
+    cache = build(2, 1024, [1024, 500], 75, v_scale=[2.0 ** power] * 2)
+    q = queries(tq, 2 * group, 1)
+    o, lse = torch.empty_like(q), torch.empty(2 * group, tq, device="cuda")
+    nv.kv_window_attention(cache, [0, 1], [1024, 500], q, scale, o, lse_out=lse)
+    k, v = (torch.cat(t) for t in zip(held(cache, 0, 1024), held(cache, 1, 500)))
+    ro, rl, tol, ltol = reference(q, k, v * 2.0 ** -power, torch.ones(tq, 1524, dtype=torch.bool), scale)
+    assert_close(o.double() * 2.0 ** -power, lse, (ro, rl, tol + 2.0 ** (-134 - power), ltol))

@@ -448,14 +448,12 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
 
 // Checks of a window's HOST lists; min_slots is 0 where the window may be empty.
 static nvfp4_status check_window(const nvfp4_kv_cache* cache, const int32_t* slots_host, const int32_t* tokens_host,
-                                 int32_t n_slots, int32_t min_slots, int64_t* total) {
+                                 int32_t n_slots, int32_t min_slots) {
   if (n_slots < min_slots || n_slots > nvfp4::kMaxWindowSlots) return NVFP4_ERR_INVALID_ARG;
   if (n_slots > 0 && (!slots_host || !tokens_host)) return NVFP4_ERR_INVALID_ARG;
-  *total = 0;
   for (int i = 0; i < n_slots; ++i) {
     if (slots_host[i] < 0 || slots_host[i] >= cache->max_chunks) return NVFP4_ERR_INVALID_ARG;
     if (tokens_host[i] < 1 || tokens_host[i] > cache->chunk_tokens) return NVFP4_ERR_SHAPE;
-    *total += tokens_host[i];
   }
   return NVFP4_OK;
 }
@@ -486,8 +484,7 @@ static nvfp4_status attention(nvfp4::AttentionArgs& a, const nvfp4_kv_cache* cac
   if (!at || at->reserved != 0 || ((!q || !o_out) && tq > 0)) return NVFP4_ERR_INVALID_ARG;
   // the kernels number the cache's tokens in 32 bits
   if (cache->head_dim != 128 || cache->chunk_tokens * cache->max_chunks > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
-  int64_t total = 0;
-  if ((st = check_window(cache, slots_host, tokens_host, n_slots, min_slots, &total)) != NVFP4_OK) return st;
+  if ((st = check_window(cache, slots_host, tokens_host, n_slots, min_slots)) != NVFP4_OK) return st;
   if (tq < 0 || q_heads < cache->heads || q_heads % cache->heads != 0 || cache->heads > 65535) return NVFP4_ERR_SHAPE;
   if (tq > nvfp4::kMaxAttentionRows / (q_heads / cache->heads)) return NVFP4_ERR_SHAPE;
   const int64_t width = (int64_t)q_heads * 128;

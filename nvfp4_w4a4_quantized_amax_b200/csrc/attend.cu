@@ -721,8 +721,6 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
   p.off_mu = c.off_mu;
   p.off_gscale = c.off_gscale;
   p.off_tokens = c.off_tokens;
-  p.slot_codes = c.slot_codes_bytes;
-  p.slot_scales = c.slot_scales_bytes;
   p.chunk = c.chunk_tokens;
   p.heads = c.heads;
   p.group = a.q_heads / c.heads;

@@ -34,7 +34,6 @@ constexpr float kLazy = 4.0f, kUp = 10.0f;
 struct Params {
   const uint8_t* base;
   int64_t off_k_codes, off_v_codes, off_k_scales, off_v_scales, off_mu, off_gscale, off_tokens;
-  int64_t slot_codes, slot_scales;
   int64_t chunk;  // tokens of a slot
   int32_t heads, group;  // cache heads, query heads of each
   FastDiv by_group;

@@ -92,10 +92,11 @@ __device__ __forceinline__ int tile_key(int n) { return (n >> 1) + 4 * (n & 1); 
 // 2 c + 1 (and + 8); nibbles of two keys are interleaved before the conversion, which then yields
 // the pairs the product wants.  P^T comes from S^T by one 8 x 8 transpose a tile.
 // A loop step takes the scores of one step of keys and the output of the step before: one alone
-// leaves a scheduler's three or four warps waiting for their own latencies.  That takes registers, so
-// three CTAs an SM (168) and not four: 1 query x 24 heads x 32768 keys 44 us with the join, 50 with
-// one step at a time and four CTAs, 51 with both in 128 registers (two CTAs and not three for 16 rows:
-// 16 x 8 heads x 16384 keys 22 and 26).  Bound by the copies and the decoding together: the copies
+// leaves a scheduler's few warps waiting for their own latencies.  That takes registers, so three CTAs
+// an SM (168) and not four: 1 query x 24 heads x 32768 keys 44 us with the join, 51 with one step at a
+// time and four CTAs, 51 with both in 128 registers.  16 rows take two CTAs (255) and not three: 16 x 8
+// heads x 16384 keys 22.4 us against 25.5, 32 x 8 x 4096 16.7 against 19.7, but 12 x 24 x 32768 65 against
+// 61.5, and 104 against 86 with a cap.  Bound by the copies and the decoding together: the copies
 // alone take 31 to 35, half as much again as their codes without the 8-byte pieces of scales.
 template <bool kExtras, int kTiles>  // kExtras: a cap, a bias or documents
 __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_kernel(const __grid_constant__ Params p) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kTiles == 1 ? 3 : 2) attend_rows_ker
   uint32_t pb[2][kTiles][2] = {};
   uint32_t keep = 0;
   // The scores of one step and the output of the step before it: two independent chains, which hide
-  // each other's latencies (there are four warps to a scheduler).
+  // each other's latencies (a scheduler has three warps, with 16 rows two).
   auto products = [&](const Stage& now, const Stage& before, auto scores, auto output) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -637,8 +638,8 @@ constexpr int kSms = 148;
 // Up to kRows rows a cache head take CTAs of few rows, above kMostRows tiles of 128; in between, where
 // CTAs of few rows decode the window more than once but start sooner, and for the number of CTAs
 // that share a window, the least of a model of the time decides, with constants from B200
-// (us, high for few rows, which no choice depends on: 0.7 of them moved no case by 10 %): a step of 32 keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its
-// SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
+// (us, high for few rows, which no choice depends on: 0.7 of them moved no case by 10 %): a step of 32
+// keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
 // besides; joining is another launch, 5, the partial results' traffic and 0.04 a part.
 AttentionPlan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   AttentionPlan best = {};

@@ -26,9 +26,11 @@ using namespace tc;
 //   kPair:  256 rows; both tiles take every step, so a decoded step feeds 256 rows.
 //   !kPair: up to 128 rows; tile t takes the steps t, t + 2, ... and the two results are joined at
 //           the end.
-// 1024 queries x 24 heads x 32768 keys: 437 to 450 us, 920 TFLOP/s; no unit is above 47 % busy, and a
+// 1024 queries x 24 heads x 32768 keys: 447 us, 920 TFLOP/s; no unit is above 47 % busy, and a
 // step takes what a tile's chain takes (softmax about 1600 cycles for 64 keys, 550 from its weights
-// to the next scores).  With a cap 706, with a bias 742; up to 128 queries about 72.
+// to the next scores).  With a bias 744; with a cap 720 where scores stay within 0.625 of it, 1020
+// where each warp's steps hold one beyond (tanh2's second form, 16 scores at a time); up to 128
+// queries about 75.
 // Both operands of both products are in the 128-byte swizzle: K~ as rows of keys (K-major), V~
 // the same way, which for O += P V~ is the MN-major B operand, so one decoder writes both.
 constexpr int kThreads = 640;

@@ -243,11 +243,12 @@ __device__ __forceinline__ float row_factor(const NormParams& p, double v, doubl
   return *shared_r;
 }
 
-// Three CTAs of 256 threads an SM (85 registers; two for FP32, whose rows take twice as many): a
-// row's reads, reduction and encoding follow one another within a CTA, so others have to fill in
-// (8192 x 9216 with residual, plain loads: two CTAs 122 us, three 107, four 117, five 135).  Bound by
-// HBM with the encoding's instructions close behind: 90 us for 495 MB (5.5 TB/s; without the encoding
-// 78).
+// Registers for three CTAs of 256 threads an SM (80; two for FP32, whose rows take twice as many): a
+// row's reads, reduction and encoding follow one another within a CTA, so others have to fill in.
+// 9216 columns take CTAs of 192 threads, four of which fit; with the plain loads, 8192 x 9216 with
+// residual took 122 us in registers for two CTAs of 256 threads, 107 for three, 117 for four, 135 for
+// five.  Bound by HBM with the encoding's instructions close behind: 91 us for 495 MB (5.4 TB/s; without
+// the encoding 78).  FP32 206 us for 949 MB; 8192 x 3072 45 us for 165 MB in bf16, 85 for 316 in FP32.
 template <bool kBf16, bool kMma, int kMode, int kLanes, bool kPipe>
 __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) norm_kernel(NormParams p) {
   extern __shared__ __align__(128) uint8_t rows_smem[];

@@ -373,9 +373,9 @@ nvfp4_status kv_window_context(const nvfp4_kv_cache* cache, const int32_t* slots
  * a row (exact for elements down to 2^-29 of the row's largest), weights times their
  * slot's g_V are rounded by at most 2^-11 of their value (2^-35 of the row's largest such
  * product where they are small: slots whose g_V lie 10^6 apart keep fewer digits of the
- * small one's part of an output); softmax statistics and lse are FP32.  A slot whose g_V is below 2^-60 of the
- * window's largest counts as zero values.  A query with a NaN or Inf gives NaN in its own
- * row, O and lse, where it sees a key.
+ * small one's part of an output); softmax statistics and lse are FP32.  A slot whose g_V
+ * is below 2^-60 of the window's largest counts as zero values.  A query with a NaN or Inf
+ * gives NaN in its own row, O and lse, where it sees a key.
  *   scale    : finite; scores have to be FP32 numbers.
  *   softcap  : 0 (none) or positive and finite; caps above 2^64 act as 2^64 (which leaves scores
  *              below 2^52 as they are), caps below 2^-30 as 2^-30.

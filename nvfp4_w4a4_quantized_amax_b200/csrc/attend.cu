@@ -637,10 +637,11 @@ constexpr int kSms = 148;
 
 // Up to kRows rows a cache head take CTAs of few rows, above kMostRows tiles of 128; in between, where
 // CTAs of few rows decode the window more than once but start sooner, and for the number of CTAs
-// that share a window, the least of a model of the time decides, with constants from B200
-// (us, high for few rows, which no choice depends on: 0.7 of them moved no case by 10 %): a step of 32
-// keys takes a warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its SM, a CTA 5 besides; a step of 64 keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14
-// besides; joining is another launch, 5, the partial results' traffic and 0.04 a part.
+// that share a window, the least of a model of the time decides, with constants from B200 (us, high for
+// few rows, which no choice depends on: 0.7 of them moved no case by 10 %): a step of 32 keys takes a
+// warp 1.8 (2.2 with 16 rows) and 0.12 (0.18) for each warp on its SM, a CTA 5 besides; a step of 64
+// keys takes a tile's CTA 1.2 (two tiles) or 0.65, a CTA 14 besides; joining is another launch, 5, the
+// partial results' traffic and 0.04 a part.
 AttentionPlan make_plan(const int32_t* tokens, int n_slots, int heads, int64_t rows) {
   AttentionPlan best = {};
   double best_us = 0.0;
